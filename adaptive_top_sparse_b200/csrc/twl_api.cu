@@ -8,7 +8,10 @@
 
 #include "twl_common.cuh"
 #include "twl_kernels.h"
+#include "twl_pages.h"
+#include "twl_prefill.h"
 #include "twl_step.h"
+#include "twl_window.h"
 
 namespace twl {
 
@@ -88,6 +91,31 @@ twl_status check_budget(int budget_pages, int budget_div, int max_budget, int ma
   return TWL_OK;
 }
 
+// Arguments of attention under a window with sinks.
+twl_status check_window(int sinks, int window, float sm_scale) {
+  if (sinks < 0 || window < 1 || !(sm_scale > 0.f) || isinf(sm_scale)) return TWL_ERR_INVALID_ARG;
+  return TWL_OK;
+}
+
+twl_status check_pools(const twl_page_pool* pools, int num_pools, const void* table, int batch,
+                       int max_pages, int num_phys, pages::Pools* out) {
+  if (!pools || !table || num_pools < 1 || num_pools > TWL_MAX_POOLS || batch < 1 ||
+      max_pages < 1 || num_phys < 1 || !aligned(table, 4))
+    return TWL_ERR_INVALID_ARG;
+  if (batch > pages::kMaxBatch || max_pages > kMaxPages || num_phys > pages::kMaxPool)
+    return TWL_ERR_UNSUPPORTED;
+  for (int i = 0; i < num_pools; ++i) {
+    if (!pools[i].data || !aligned(pools[i].data, 16) || pools[i].page_bytes < 16 ||
+        pools[i].page_bytes % 16 != 0)
+      return TWL_ERR_INVALID_ARG;
+    out->pool[i] = pools[i];
+  }
+  out->count = num_pools;
+  return TWL_OK;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
 twl_status check_ws(void* ws, size_t ws_bytes, size_t need) {
   if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return TWL_ERR_WORKSPACE;
   return TWL_OK;
@@ -165,7 +193,6 @@ extern "C" {
 size_t twl_workspace_bytes(int32_t op, int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                            int32_t max_pages, int32_t max_budget, int32_t rows,
                            int32_t row_stride) {
-  (void)rows;
   if (batch < 0 || num_q_heads < 0 || num_kv_heads < 0 || max_pages < 0 || max_budget < 0 ||
       row_stride < 0)
     return 0;
@@ -194,6 +221,19 @@ size_t twl_workspace_bytes(int32_t op, int32_t batch, int32_t num_q_heads, int32
       c.take<char>(decode_step_ws_bytes(batch, num_q_heads, num_kv_heads, max_pages,
                                          max_budget));
       break;
+    case TWL_OP_WINDOW_DECODE:
+    case TWL_OP_INT4_DECODE:
+      if (num_kv_heads < 1 || num_q_heads < num_kv_heads) return 0;
+      c.take<char>(window::workspace_bytes(batch, num_q_heads, num_kv_heads));
+      break;
+    case TWL_OP_WINDOW_PREFILL:
+      if (num_kv_heads < 1 || num_q_heads < num_kv_heads) return 0;
+      c.take<char>(prefill::workspace_bytes(batch, num_q_heads, num_kv_heads));
+      break;
+    case TWL_OP_PAGES:
+      if (rows < 0) return 0;
+      c.take<char>(pages::workspace_bytes(batch, max_pages, rows));
+      break;
     default:
       return 0;
   }
@@ -216,6 +256,7 @@ twl_status twl_device_status(void* ws, uint32_t* flags, int32_t clear, twl_strea
   if (clear && cudaMemsetAsync(ws, 0, sizeof(uint32_t), s) != cudaSuccess) return TWL_ERR_CUDA;
   if (h & TWL_FLAG_BAD_INDEX) return TWL_ERR_BAD_INDEX;
   if (h & TWL_FLAG_TIMEOUT) return TWL_ERR_TIMEOUT;
+  if (h & TWL_FLAG_NO_PAGES) return TWL_ERR_NO_PAGES;
   return TWL_OK;
 }
 
@@ -229,6 +270,7 @@ const char* twl_status_string(twl_status s) {
     case TWL_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case TWL_ERR_BAD_INDEX: return "page table, sequence length or index list out of range";
     case TWL_ERR_SCRATCH_LIMIT: return "request exceeds the built-in scratch of the no-allocation call";
+    case TWL_ERR_NO_PAGES: return "the page-table step wants more pages than are free";
     default: return "unknown status";
   }
 }
@@ -513,6 +555,186 @@ twl_status twl_decode_step(const void* q, int32_t num_q_heads, const twl_paged_k
   }
   step::carve(a, sws, pl, k.batch, num_q_heads, k.hkv, k.max_pages);
   return cuda_status(step::launch(a, pl, (cudaStream_t)stream));
+}
+
+twl_status twl_window_decode(const void* q, int32_t num_q_heads, const twl_paged_kv* kv,
+                             int32_t sinks, int32_t window, float sm_scale, float* o, float* lse,
+                             void* ws, size_t ws_bytes, twl_stream_t stream) {
+  KV k;
+  twl_status st = check_kv(kv, true, true, &k);
+  if (st != TWL_OK) return st;
+  if ((st = check_heads(num_q_heads, k.hkv)) != TWL_OK) return st;
+  if ((st = check_window(sinks, window, sm_scale)) != TWL_OK) return st;
+  if (!q || !o || !lse || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4))
+    return TWL_ERR_INVALID_ARG;
+  if ((long long)k.batch * k.hkv > 4096) return TWL_ERR_UNSUPPORTED;
+  Carve c{static_cast<char*>(ws)};
+  void* body = c.take<char>(window::workspace_bytes(k.batch, num_q_heads, k.hkv));
+  if ((st = check_ws(ws, ws_bytes, c.off)) != TWL_OK) return st;
+  window::Args a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.hq = num_q_heads;
+  a.k = k.k;
+  a.v = k.v;
+  a.page_table = k.page_table;
+  a.seq_lens = const_cast<int*>(k.seq_lens);  // read only: nothing is appended
+  a.batch = k.batch;
+  a.hkv = k.hkv;
+  a.max_pages = k.max_pages;
+  a.num_phys = k.num_phys;
+  a.sinks = sinks;
+  a.window = window;
+  a.scale_log2 = sm_scale * kLog2e;
+  a.o = o;
+  a.lse = lse;
+  a.flags = flags_of(ws);
+  window::carve(a, body);
+  return cuda_status(window::launch(a, (cudaStream_t)stream));
+}
+
+twl_status twl_window_prefill(const void* q, const int32_t* q_start, int32_t total_q,
+                              int32_t num_q_heads, const twl_paged_kv* kv, int32_t sinks,
+                              int32_t window, float sm_scale, void* o, float* lse, void* ws,
+                              size_t ws_bytes, twl_stream_t stream) {
+  KV k;
+  twl_status st = check_kv(kv, true, true, &k);
+  if (st != TWL_OK) return st;
+  if ((st = check_heads(num_q_heads, k.hkv)) != TWL_OK) return st;
+  if ((st = check_window(sinks, window, sm_scale)) != TWL_OK) return st;
+  if (total_q < 0 || !q_start || !aligned(q_start, 4)) return TWL_ERR_INVALID_ARG;
+  if (total_q > 0 && (!q || !o || !lse || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4)))
+    return TWL_ERR_INVALID_ARG;
+  if ((long long)k.batch * k.hkv > 4096) return TWL_ERR_UNSUPPORTED;
+  Carve c{static_cast<char*>(ws)};
+  void* body = c.take<char>(prefill::workspace_bytes(k.batch, num_q_heads, k.hkv));
+  if ((st = check_ws(ws, ws_bytes, c.off)) != TWL_OK) return st;
+  if (total_q == 0) return TWL_OK;
+  prefill::Args a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_start = q_start;
+  a.total_q = total_q;
+  a.hq = num_q_heads;
+  a.k = k.k;
+  a.v = k.v;
+  a.page_table = k.page_table;
+  a.seq_lens = k.seq_lens;
+  a.batch = k.batch;
+  a.hkv = k.hkv;
+  a.max_pages = k.max_pages;
+  a.num_phys = k.num_phys;
+  a.sinks = sinks;
+  a.window = window;
+  a.scale_log2 = sm_scale * kLog2e;
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  a.flags = flags_of(ws);
+  return cuda_status(prefill::launch(a, body, (cudaStream_t)stream));
+}
+
+twl_status twl_int4_decode(const void* q, int32_t num_q_heads, const twl_int4_kv* kv,
+                           const void* k_new, const void* v_new, int32_t advance, int32_t sinks,
+                           int32_t window, float sm_scale, float* o, float* lse, void* ws,
+                           size_t ws_bytes, twl_stream_t stream) {
+  if (!kv) return TWL_ERR_INVALID_ARG;
+  // the same checks of shapes and pointers as an fp16 cache
+  const twl_paged_kv shape = {kv->k,           kv->v,           kv->page_table, kv->seq_lens,
+                              kv->batch,       kv->num_kv_heads, kv->head_dim,  kv->page_size,
+                              kv->max_pages,   kv->num_phys_pages};
+  KV k;
+  twl_status st = check_kv(&shape, true, true, &k);
+  if (st != TWL_OK) return st;
+  if ((st = check_heads(num_q_heads, k.hkv)) != TWL_OK) return st;
+  if ((st = check_window(sinks, window, sm_scale)) != TWL_OK) return st;
+  if (!kv->k_scale_zero || !kv->v_scale_zero || !aligned(kv->k_scale_zero, 16) ||
+      !aligned(kv->v_scale_zero, 16) || !q || !o || !lse || !aligned(q, 16) || !aligned(o, 16) ||
+      !aligned(lse, 4))
+    return TWL_ERR_INVALID_ARG;
+  if (!k_new != !v_new || (advance && !k_new) || !aligned(k_new, 16) || !aligned(v_new, 16))
+    return TWL_ERR_INVALID_ARG;
+  if ((long long)k.batch * k.hkv > 4096) return TWL_ERR_UNSUPPORTED;
+  Carve c{static_cast<char*>(ws)};
+  void* body = c.take<char>(window::workspace_bytes(k.batch, num_q_heads, k.hkv));
+  if ((st = check_ws(ws, ws_bytes, c.off)) != TWL_OK) return st;
+  window::Args a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.hq = num_q_heads;
+  a.kc = static_cast<uint8_t*>(kv->k);
+  a.vc = static_cast<uint8_t*>(kv->v);
+  a.ksz = static_cast<uint32_t*>(kv->k_scale_zero);
+  a.vsz = static_cast<uint32_t*>(kv->v_scale_zero);
+  a.k_new = static_cast<const uint16_t*>(k_new);
+  a.v_new = static_cast<const uint16_t*>(v_new);
+  a.page_table = k.page_table;
+  a.seq_lens = kv->seq_lens;
+  a.batch = k.batch;
+  a.hkv = k.hkv;
+  a.max_pages = k.max_pages;
+  a.num_phys = k.num_phys;
+  a.sinks = sinks;
+  a.window = window;
+  a.appended = k_new ? 1 : 0;
+  a.advance = advance ? 1 : 0;
+  a.scale_log2 = sm_scale * kLog2e;
+  a.o = o;
+  a.lse = lse;
+  a.flags = flags_of(ws);
+  window::carve(a, body);
+  return cuda_status(window::launch(a, (cudaStream_t)stream));
+}
+
+twl_status twl_remap_pages(const twl_page_pool* pools, int32_t num_pools, int32_t* page_table,
+                           int32_t* seq_lens, int32_t batch, int32_t max_pages,
+                           int32_t num_phys_pages, const int32_t* parent, const int32_t* reserve,
+                           int32_t sinks, int32_t window, void* ws, size_t ws_bytes,
+                           twl_stream_t stream) {
+  pages::Pools p;
+  twl_status st =
+      check_pools(pools, num_pools, page_table, batch, max_pages, num_phys_pages, &p);
+  if (st != TWL_OK) return st;
+  if (!seq_lens || !parent || !aligned(seq_lens, 4) || !aligned(parent, 4) ||
+      !aligned(reserve, 4) || sinks < 0 || window < 1)
+    return TWL_ERR_INVALID_ARG;
+  Carve c{static_cast<char*>(ws)};
+  void* body = c.take<char>(pages::workspace_bytes(batch, max_pages, num_phys_pages));
+  if ((st = check_ws(ws, ws_bytes, c.off)) != TWL_OK) return st;
+  pages::Args a = {};
+  a.table = page_table;
+  a.seq_lens = seq_lens;
+  a.parent = parent;
+  a.reserve = reserve;
+  a.batch = batch;
+  a.max_pages = max_pages;
+  a.num_phys = num_phys_pages;
+  a.sinks = sinks;
+  a.window = window;
+  a.flags = flags_of(ws);
+  pages::carve(a, body);
+  return cuda_status(pages::launch_remap(a, p, (cudaStream_t)stream));
+}
+
+twl_status twl_compact_pages(const twl_page_pool* pools, int32_t num_pools,
+                             const int32_t* page_table, int32_t* page_table_out, int32_t batch,
+                             int32_t max_pages, int32_t num_phys_pages, int32_t* num_used,
+                             void* ws, size_t ws_bytes, twl_stream_t stream) {
+  pages::Pools p;
+  twl_status st =
+      check_pools(pools, num_pools, page_table, batch, max_pages, num_phys_pages, &p);
+  if (st != TWL_OK) return st;
+  if (!page_table_out || !num_used || !aligned(page_table_out, 4) || !aligned(num_used, 4))
+    return TWL_ERR_INVALID_ARG;
+  Carve c{static_cast<char*>(ws)};
+  void* body = c.take<char>(pages::workspace_bytes(batch, max_pages, num_phys_pages));
+  if ((st = check_ws(ws, ws_bytes, c.off)) != TWL_OK) return st;
+  pages::Args a = {};
+  a.table = const_cast<int*>(page_table);  // read only unless it is page_table_out
+  a.table_out = page_table_out;
+  a.num_used = num_used;
+  a.batch = batch;
+  a.max_pages = max_pages;
+  a.num_phys = num_phys_pages;
+  a.flags = flags_of(ws);
+  pages::carve(a, body);
+  return cuda_status(pages::launch_compact(a, p, (cudaStream_t)stream));
 }
 
 void twl_test_set_waits(uint32_t max_polls, int32_t stall_estimate) {

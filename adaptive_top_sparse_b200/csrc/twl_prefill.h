@@ -1,0 +1,30 @@
+// Attention of chunks of many tokens over a window with sinks (twl_prefill.cu): arguments, launch.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace twl {
+namespace prefill {
+
+struct Args {
+  const uint16_t* q;   // [total_q][hq][128]
+  const int* q_start;  // [batch + 1]
+  int total_q, hq;
+  const uint16_t *k, *v;
+  const int* page_table;
+  const int* seq_lens;
+  int batch, hkv, max_pages, num_phys;
+  int sinks, window;
+  float scale_log2;  // score scale * log2(e)
+  uint16_t* o;       // [total_q][hq][128]
+  float* lse;        // [total_q][hq]
+  uint32_t* flags;
+};
+
+size_t workspace_bytes(int batch, int hq, int hkv);
+cudaError_t launch(const Args& a, void* ws, cudaStream_t s);
+
+}  // namespace prefill
+}  // namespace twl

@@ -1,0 +1,715 @@
+// Attention of one query token per sequence over a sliding window and the first (sink) tokens of
+// its paged cache: fp16 K/V, or K and V held in 4 bits.
+//
+// Query at position t = n - 1 sees key j iff j < n and (j < sinks or j >= n - window).  With
+// s_j = scale q.k_j:  o = sum_j 2^(s_j' - m) v_j / sum_j 2^(s_j' - m),  s' = s log2(e).  A 4-bit
+// row is x = c s + z (codes c, scale s, zero z of the row), so
+//   q.k = s_k (q.c) + z_k sum(q)   and   sum_j p_j v_j = sum_j (p_j s_v,j) c_j + sum_j p_j z_v,j:
+// only the integer codes go through the tensor cores, never a dequantised row.
+//
+// Bound: memory.  A token of one kv-head is 512 B (fp16) or 136 B (4-bit) and every byte is read
+// once; the heads of a GQA group share the read.
+//
+// Work split: a page of 16 tokens of one (sequence, kv-head) group is a tile; the visible tiles of
+// all groups form one flat list that is cut into equal runs, one per CTA, whatever the lengths.  A
+// group that lies inside one run is finished there; a group cut by runs leaves one partial (max,
+// sum, o) per CTA, and the CTA that arrives last merges them in CTA order (so the result does not
+// depend on who is last).  Lengths stay on the device: each CTA derives the list from seq_lens.
+//
+// Inside a CTA the warps take the tiles in turn, each through its own ring of cp.async stages (no
+// barrier in the loop), with transposed products so that the <= 8 heads of a group are the N = 8
+// of mma.m16n8k16:  S^T = K Q^T (16 tokens x 8 heads), O^T = V^T P^T (16 dims x 8 heads); P^T
+// comes from S^T by an 8x8 transpose in registers (movmatrix).
+// Precision: o and lse are fp32 results, so P enters as hi + lo fp16 parts (22 bits).  With G <= 4
+// the parts use the two halves of the N = 8 columns and cost nothing; G = 8 takes two products.
+#include "twl_common.cuh"
+#include "twl_kernels.h"
+#include "twl_quant.cuh"
+#include "twl_window.h"
+
+namespace twl {
+namespace window {
+namespace {
+
+constexpr float kLn2 = 0.69314718055994530942f;
+// The running maximum of a head is only raised when a score exceeds it by more than this (log2
+// units): weights stay below 2^8, far from fp16's largest value, and most tiles skip the rescale.
+constexpr float kSlack = 8.f;
+// Where a 4-bit code meets the tensor core as fp16 (see k_window_decode): two per word.
+constexpr uint32_t kHigh = 0x07800780u, kLow = 0x00F000F0u;
+constexpr int kPartStride = 132;  // floats of one head's partial: o[128], max, sum, pad
+
+template <bool INT4>
+struct Cfg;
+template <>
+struct Cfg<false> {
+  static constexpr int kWarps = 8, kStages = 3, kTile = 8192, kRegs = 36;
+};
+template <>
+struct Cfg<true> {
+  static constexpr int kWarps = 16, kStages = 5, kTile = 2176, kRegs = 38;
+};
+
+template <bool INT4>
+constexpr size_t smem_bytes(int batch) {
+  using C = Cfg<INT4>;
+  return (size_t)C::kWarps * C::kStages * C::kTile + (size_t)(C::kWarps / 2) * C::kRegs * 128 +
+         (size_t)(batch + 1) * 4;
+}
+
+// A (sequence, kv-head) group and its tiles [gs, ge) of the flat list.
+struct Group {
+  int b, kvh, gs, ge;
+  int n, lo;     // keys; first key of the window
+  int sink_pages, first_page;  // sink pages before the window's first page
+};
+
+__device__ __forceinline__ Group group_of(const Args& a, const int* prefix, int f) {
+  int x = 0, y = a.batch;  // prefix[x] * hkv <= f < prefix[y] * hkv
+  while (y - x > 1) {
+    const int mid = (x + y) >> 1;
+    if ((long long)prefix[mid] * a.hkv <= f) x = mid;
+    else y = mid;
+  }
+  Group g;
+  g.b = x;
+  const int per = prefix[x + 1] - prefix[x];
+  g.kvh = (f - prefix[x] * a.hkv) / per;
+  g.gs = prefix[x] * a.hkv + g.kvh * per;
+  g.ge = g.gs + per;
+  g.n = a.seq_lens[x] + a.appended;
+  g.lo = max(0, g.n - a.window);
+  g.first_page = g.lo / kPage;
+  g.sink_pages = min((min(a.sinks, g.n) + kPage - 1) / kPage, g.first_page);
+  return g;
+}
+
+// Tiles of sequence b per kv-head; 0 for an empty slot and for one that cannot be served (flagged
+// by `report`).
+__device__ int seq_tiles(const Args& a, int b, bool report) {
+  int n = a.seq_lens[b];
+  if (a.appended) {
+    const int j = n >> 4;
+    int ph = -2;
+    if (n >= 0 && j < a.max_pages) ph = a.page_table[(size_t)b * a.max_pages + j];
+    if (n == 0 && ph == -1) return 0;  // an empty slot
+    if (ph < 0 || ph >= a.num_phys) {
+      if (report) raise_flag(a.flags, TWL_FLAG_BAD_INDEX);
+      return 0;
+    }
+    ++n;
+  }
+  if (n < 0 || n > a.max_pages * kPage) {
+    if (report) raise_flag(a.flags, TWL_FLAG_BAD_INDEX);
+    return 0;
+  }
+  if (n == 0) return 0;
+  const int first = max(0, n - a.window) / kPage;
+  return min((min(a.sinks, n) + kPage - 1) / kPage, first) + (n + kPage - 1) / kPage - first;
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+// 16-byte slot of chunk c (0..3) of row r of a 4-bit V tile.  A lane reads 8 bytes of the rows of
+// its four tokens (2t, 2t + 1, 2t + 8, 2t + 9); with this placement the 16 lanes of one shared
+// memory phase touch every bank once.
+__device__ __forceinline__ int v_slot(int r, int c) {
+  return (r >> 1) * 8 + (((r ^ (r >> 2)) & 1) << 2) + (c ^ (r & 2));
+}
+
+// (c - 8) 2^-9 of two codes whose fp16 values are c 2^-9 / up.
+__device__ __forceinline__ uint32_t centre(uint32_t codes, float up) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&codes), __float2half2_rn(up),
+                            __float2half2_rn(-0x1p-6f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Softmax state and output accumulators of a warp.  Lane (g, t) = (lane / 4, lane % 4) holds the
+// heads (N columns) 2t and 2t + 1; m is the same over g, l and z are this lane's tokens only.
+struct State {
+  float m[2], l[2], z[2], acc[8][4];
+};
+
+__device__ __forceinline__ void reset(State& st) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) st.m[c] = -INFINITY, st.l[c] = 0.f, st.z[c] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) st.acc[i][c] = 0.f;
+}
+
+__device__ __forceinline__ void scale_state(State& st, float f0, float f1) {
+  st.l[0] *= f0, st.l[1] *= f1, st.z[0] *= f0, st.z[1] *= f1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    st.acc[i][0] *= f0, st.acc[i][1] *= f1, st.acc[i][2] *= f0, st.acc[i][3] *= f1;
+  }
+}
+
+// 0 in place of -inf: the reference of a head that has seen nothing (every weight 2^(-inf) = 0).
+__device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+// Raises the maxima to cover the tile's t values (t[0], t[1]: token g, heads 2t, 2t + 1; t[2],
+// t[3]: token g + 8) when one exceeds them by more than the slack.
+__device__ __forceinline__ void update_max(State& st, const float (&t)[4]) {
+  const bool need = fmaxf(t[0], t[2]) > st.m[0] + kSlack || fmaxf(t[1], t[3]) > st.m[1] + kSlack;
+  if (!__any_sync(0xffffffffu, need)) return;
+  float f[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    float x = fmaxf(t[c], t[c + 2]);
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+    const float m = fmaxf(st.m[c], x);
+    f[c] = exp2_fast(st.m[c] - ref_of(m));
+    st.m[c] = m;
+  }
+  scale_state(st, f[0], f[1]);
+}
+
+// P^T fragments (hi and lo parts) of the weights w (same order as t in update_max).
+template <int G>
+__device__ __forceinline__ void p_fragments(const float (&w)[4], bool low, uint32_t (&hi)[2],
+                                            uint32_t (&lo)[2]) {
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const __half2 h = __floats2half2_rn(w[2 * r], w[2 * r + 1]);
+    const float2 f = __half22float2(h);
+    const __half2 d = __floats2half2_rn(w[2 * r] - f.x, w[2 * r + 1] - f.y);
+    const uint32_t hb = *reinterpret_cast<const uint32_t*>(&h);
+    const uint32_t db = *reinterpret_cast<const uint32_t*>(&d);
+    if constexpr (G == 8) {
+      hi[r] = transpose8(hb);
+      lo[r] = transpose8(db);
+    } else {  // columns 0-3 carry the hi parts, 4-7 (lanes t >= 2) the lo parts of the same heads
+      hi[r] = transpose8(low ? db : hb);
+    }
+  }
+}
+
+template <int G, bool INT4>
+__global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
+    k_window_decode(const __grid_constant__ Args a) {
+  using C = Cfg<INT4>;
+  constexpr int kWarps = C::kWarps, kStages = C::kStages, kTile = C::kTile, kBufs = kWarps / 2;
+  extern __shared__ __align__(128) unsigned char smem[];
+  unsigned char* ring = smem;
+  float* buf = reinterpret_cast<float*>(smem + (size_t)kWarps * kStages * kTile);
+  int* prefix = reinterpret_cast<int*>(buf + kBufs * C::kRegs * 32);
+  __shared__ int scan_sh[33];
+  __shared__ int tile_base[kWarps][kStages];  // first token of a stage's page, or -1: no page
+  __shared__ int is_last;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lg = lane >> 2, lt = lane & 3;
+
+  // ---- the flat list: prefix[b] = tiles per kv-head of the sequences before b
+  int carry = 0;
+  for (int base = 0; base < a.batch; base += blockDim.x) {
+    const int b = base + tid;
+    const int c = b < a.batch ? seq_tiles(a, b, blockIdx.x == 0) : 0;
+    int total;
+    const int ex = block_exclusive_scan(c, scan_sh, &total);
+    if (b < a.batch) prefix[b] = carry + ex;
+    carry += total;
+  }
+  if (tid == 0) prefix[a.batch] = carry;
+  __syncthreads();
+  const int total = prefix[a.batch] * a.hkv;
+
+  // ---- sequences with no visible key
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    if (prefix[b + 1] != prefix[b]) continue;
+    for (int i = tid; i < a.hq * kHeadDim; i += blockDim.x)
+      a.o[(size_t)b * a.hq * kHeadDim + i] = 0.f;
+    for (int i = tid; i < a.hq; i += blockDim.x) a.lse[(size_t)b * a.hq + i] = -INFINITY;
+  }
+
+  const int runs = min((int)gridDim.x, total);
+  const int run = blockIdx.x;
+  if (run < runs) {
+    const int f0 = (int)((long long)total * run / runs);
+    const int f1 = (int)((long long)total * (run + 1) / runs);
+    unsigned char* my_ring = ring + (size_t)warp * kStages * kTile;
+
+    // ---- loads: tile lf goes to stage ls; its page id is fetched one tile ahead
+    int lf = f0 + warp, ls = 0;
+    Group lgp = group_of(a, prefix, min(lf, f1 - 1));
+    auto page_of = [&](const Group& g, int f) {
+      const int i = f - g.gs;
+      return i < g.sink_pages ? i : g.first_page + i - g.sink_pages;
+    };
+    auto fetch_phys = [&]() {
+      if (lf >= f1) return -1;
+      if (lf >= lgp.ge) lgp = group_of(a, prefix, lf);
+      return a.page_table[(size_t)lgp.b * a.max_pages + page_of(lgp, lf)];
+    };
+    int phys = fetch_phys();
+    auto issue = [&]() {
+      if (lf < f1) {
+        const int base = page_of(lgp, lf) * kPage;
+        const bool ok = phys >= 0 && phys < a.num_phys;
+        if (lane == 0) {
+          tile_base[warp][ls] = ok ? base : -1;
+          if (!ok) raise_flag(a.flags, TWL_FLAG_BAD_INDEX);
+        }
+        unsigned char* st = my_ring + ls * kTile;
+        const size_t row0 = ok ? ((size_t)phys * a.hkv + lgp.kvh) * kPage : 0;
+        if constexpr (INT4) {
+#pragma unroll
+          for (int it = 0; it < 2; ++it) {
+            const int r = it * 8 + (lane >> 2), c = lane & 3;
+            cp_async16(st + r * 64 + c * 16, a.kc + (row0 + r) * 64 + c * 16, ok);
+            cp_async16(st + 1024 + v_slot(r, c) * 16, a.vc + (row0 + r) * 64 + c * 16, ok);
+          }
+          if (lane < 8) {
+            const uint32_t* src = (lane < 4 ? a.ksz : a.vsz) + row0 + 4 * (lane & 3);
+            cp_async16(st + 2048 + lane * 16, src, ok);
+          }
+        } else {
+          const int c = lane & 15;
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int r = it * 2 + (lane >> 4), tok = base + r;
+            // rows nobody sees are zeroed: a weight of 0 times a stale infinity would be NaN
+            const bool see = ok && tok < lgp.n && (tok < a.sinks || tok >= lgp.lo);
+            const size_t off = (row0 + r) * kHeadDim + c * 8;
+            const int slot = r * 256 + ((c ^ (r & 7)) * 16);
+            cp_async16(st + slot, a.k + off, see);
+            cp_async16(st + 4096 + slot, a.v + off, see);
+          }
+        }
+        lf += kWarps;
+        phys = fetch_phys();
+      }
+      cp_async_commit();
+      ls = ls + 1 == kStages ? 0 : ls + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue();
+
+    int f = f0 + warp, cs = 0;
+    int gf = f0;  // start of the current segment
+    while (gf < f1) {
+      const Group g = group_of(a, prefix, gf);
+      const int gend = min(g.ge, f1);
+      // ---- the group's queries as the B operand: column = head (G <= 4: heads 0-3 twice)
+      uint32_t qb[16];
+      float qsum[2] = {0.f, 0.f};
+      {
+        const int h = G == 8 ? lg : (lg & 3);
+        const uint16_t* qr = a.q + ((size_t)g.b * a.hq + g.kvh * G + h) * kHeadDim;
+        const bool has = h < G;
+        if constexpr (INT4) {
+          float sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+            if (has) raw = *reinterpret_cast<const uint4*>(qr + 32 * lt + 8 * w);
+            const uint32_t p[4] = {raw.x, raw.y, raw.z, raw.w};  // channel pairs (0,1) .. (6,7)
+            qb[4 * w + 0] = __byte_perm(p[0], p[2], 0x5410);     // (0, 4)
+            qb[4 * w + 1] = __byte_perm(p[1], p[3], 0x5410);     // (2, 6)
+            qb[4 * w + 2] = __byte_perm(p[0], p[2], 0x7632);     // (1, 5)
+            qb[4 * w + 3] = __byte_perm(p[1], p[3], 0x7632);     // (3, 7)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+              sum += x.x + x.y;
+            }
+          }
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          // lane 4 h holds head h's sum; this lane needs columns 2t and 2t + 1
+          qsum[0] = __shfl_sync(0xffffffffu, sum, 4 * (2 * lt)) * a.scale_log2;
+          qsum[1] = __shfl_sync(0xffffffffu, sum, 4 * (2 * lt + 1)) * a.scale_log2;
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            qb[2 * kk] = has ? *reinterpret_cast<const uint32_t*>(qr + 16 * kk + 2 * lt) : 0u;
+            qb[2 * kk + 1] =
+                has ? *reinterpret_cast<const uint32_t*>(qr + 16 * kk + 8 + 2 * lt) : 0u;
+          }
+        }
+      }
+      State st;
+      reset(st);
+      for (; f < gend; f += kWarps) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();  // every lane's copies have landed, and the stage read last is free
+        issue();
+        unsigned char* tile = my_ring + cs * kTile;
+        const int base = tile_base[warp][cs];
+        cs = cs + 1 == kStages ? 0 : cs + 1;
+        if (base < 0) continue;
+        const int k0 = base + lg, k1 = k0 + 8;
+        const bool see0 = k0 < g.n && (k0 < a.sinks || k0 >= g.lo);
+        const bool see1 = k1 < g.n && (k1 < a.sinks || k1 >= g.lo);
+        float x[4], w[4];
+        if constexpr (INT4) {
+          uint32_t* ksz = reinterpret_cast<uint32_t*>(tile + 2048);
+          uint32_t* vsz = ksz + 16;
+          if (a.appended && (unsigned)(g.n - 1 - base) < (unsigned)kPage) {
+            // the new token's row: quantised here, kept in the cache and patched into the tile
+            const int r = (g.n - 1) & (kPage - 1);
+            const int ph = a.page_table[(size_t)g.b * a.max_pages + base / kPage];
+            const size_t row = ((size_t)ph * a.hkv + g.kvh) * kPage + r;
+            const size_t in = ((size_t)g.b * a.hkv + g.kvh) * kHeadDim + lane * 4;
+            uint32_t sz;
+            uint16_t code = quantize_row_warp(load_half4(a.k_new + in), &sz);
+            reinterpret_cast<uint16_t*>(a.kc + row * 64)[lane] = code;
+            reinterpret_cast<uint16_t*>(tile + r * 64)[lane] = code;
+            if (lane == 0) a.ksz[row] = sz, ksz[r] = sz;
+            code = quantize_row_warp(load_half4(a.v_new + in), &sz);
+            reinterpret_cast<uint16_t*>(a.vc + row * 64)[lane] = code;
+            reinterpret_cast<uint16_t*>(tile + 1024 + v_slot(r, lane >> 3) * 16)[lane & 7] = code;
+            if (lane == 0) a.vsz[row] = sz, vsz[r] = sz;
+            __syncwarp();
+          }
+          // A 4-bit code c at bits 7-10 of a half is the fp16 value c 2^-17, at bits 4-7 c 2^-20
+          // (fp16 is linear in its bits up to 2^11: subnormals and the first binade).  Not at bits
+          // 0-3: the tensor core aligns products by exponent, and ten leading zeros of a
+          // subnormal cost the sum ten bits (measured: 6e-5 instead of 1e-6 of max|v|).
+          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint4 ra = *reinterpret_cast<const uint4*>(tile + lg * 64 + lt * 16);
+          const uint4 rb = *reinterpret_cast<const uint4*>(tile + (lg + 8) * 64 + lt * 16);
+          const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0[4] = {wa[i] << 7 & kHigh, wb[i] << 7 & kHigh, wa[i] >> 1 & kHigh,
+                                    wb[i] >> 1 & kHigh};
+            const uint32_t a1[4] = {wa[i] & kLow, wb[i] & kLow, wa[i] >> 8 & kLow,
+                                    wb[i] >> 8 & kLow};
+            mma_16816(s0, a0, qb[4 * i], qb[4 * i + 1]);
+            mma_16816(s1, a1, qb[4 * i + 2], qb[4 * i + 3]);
+          }
+          float sv[2], zv[2], t[4];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t kk = ksz[lg + 8 * r], vv = vsz[lg + 8 * r];
+            const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&kk));
+            const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&vv));
+            sv[r] = vf.x, zv[r] = vf.y;
+            const float ks = kf.x * a.scale_log2;
+            // the weight that meets the codes is p s_v: its reference includes s_v's exponent, so
+            // that its fp16 parts keep their 22 bits whatever the scale of V
+            const float e = (float)((int)((vv >> 10) & 31u) - 15);
+            const bool see = r ? see1 : see0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float d = fmaf(s1[2 * r + c], 0x1p20f, s0[2 * r + c] * 0x1p17f);
+              x[2 * r + c] = fmaf(ks, d, kf.y * qsum[c]);
+              t[2 * r + c] = see ? x[2 * r + c] + e : -INFINITY;
+            }
+          }
+          update_max(st, t);
+          const float m0 = ref_of(st.m[0]), m1 = ref_of(st.m[1]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const bool see = r ? see1 : see0;
+            const float p0 = see ? exp2_fast(x[2 * r] - m0) : 0.f;
+            const float p1 = see ? exp2_fast(x[2 * r + 1] - m1) : 0.f;
+            const float ss = see ? sv[r] : 0.f;
+            const float zz = see ? fmaf(8.f, sv[r], zv[r]) : 0.f;  // codes enter as c - 8
+            st.l[0] += p0, st.l[1] += p1;
+            st.z[0] = fmaf(p0, zz, st.z[0]), st.z[1] = fmaf(p1, zz, st.z[1]);
+            w[2 * r] = p0 * ss, w[2 * r + 1] = p1 * ss;
+          }
+        } else {
+          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint32_t kb = (uint32_t)__cvta_generic_to_shared(tile);
+#pragma unroll
+          for (int kk = 0; kk < 8; kk += 2) {
+            const int r = lane & 15;
+            uint32_t fa[4], fb[4];
+            ldmatrix4(fa, kb + r * 256 + (((2 * kk + (lane >> 4)) ^ (r & 7)) * 16));
+            ldmatrix4(fb, kb + r * 256 + (((2 * kk + 2 + (lane >> 4)) ^ (r & 7)) * 16));
+            mma_16816(s0, fa, qb[2 * kk], qb[2 * kk + 1]);
+            mma_16816(s1, fb, qb[2 * kk + 2], qb[2 * kk + 3]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = (i < 2 ? see0 : see1) ? (s0[i] + s1[i]) * a.scale_log2 : -INFINITY;
+          update_max(st, x);
+          const float m0 = ref_of(st.m[0]), m1 = ref_of(st.m[1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[i] = (i < 2 ? see0 : see1) ? exp2_fast(x[i] - (i & 1 ? m1 : m0)) : 0.f;
+            st.l[i & 1] += w[i];
+          }
+        }
+        uint32_t ph[2], pl[2];
+        p_fragments<G>(w, lt >= 2, ph, pl);
+        if constexpr (INT4) {
+          const int c = lg >> 1;  // 16-byte chunk of the lane's 16 channels
+          uint2 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 2 * lt + (i & 1) + (i >> 1) * 8;
+            v[i] = *reinterpret_cast<const uint2*>(tile + 1024 + v_slot(r, c) * 16 + (lg & 1) * 8);
+          }
+          const uint32_t x4[4] = {__byte_perm(v[0].x, v[1].x, 0x5410),
+                                  __byte_perm(v[0].x, v[1].x, 0x7632),
+                                  __byte_perm(v[0].y, v[1].y, 0x5410),
+                                  __byte_perm(v[0].y, v[1].y, 0x7632)};
+          const uint32_t y4[4] = {__byte_perm(v[2].x, v[3].x, 0x5410),
+                                  __byte_perm(v[2].x, v[3].x, 0x7632),
+                                  __byte_perm(v[2].y, v[3].y, 0x5410),
+                                  __byte_perm(v[2].y, v[3].y, 0x7632)};
+          // Block i: row g = channel 16 g + 2 i, row g + 8 = 16 g + 2 i + 1.  The codes enter as
+          // (c - 8) 2^-9: without the offset the sum of codes and the sum of zeros are both far
+          // larger than a diffuse head's o, and their difference is not an fp32 result any more
+          // (measured at 8K tokens: 2e-5 of |o| off instead of 2e-6).
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t xx = i & 1 ? x4[i >> 1] >> 8 : x4[i >> 1];
+            const uint32_t yy = i & 1 ? y4[i >> 1] >> 8 : y4[i >> 1];
+            const uint32_t av[4] = {centre(xx & 0x000F000Fu, 0x1p15f), centre(xx & kLow, 0x1p11f),
+                                    centre(yy & 0x000F000Fu, 0x1p15f), centre(yy & kLow, 0x1p11f)};
+            mma_16816(st.acc[i], av, ph[0], ph[1]);
+            if constexpr (G == 8) mma_16816(st.acc[i], av, pl[0], pl[1]);
+          }
+        } else {
+          const uint32_t vb = (uint32_t)__cvta_generic_to_shared(tile) + 4096;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = (lane >> 4) * 8 + (lane & 7);
+            uint32_t av[4];
+            ldmatrix4_trans(av, vb + r * 256 + (((2 * i + ((lane >> 3) & 1)) ^ (r & 7)) * 16));
+            mma_16816(st.acc[i], av, ph[0], ph[1]);
+            if constexpr (G == 8) mma_16816(st.acc[i], av, pl[0], pl[1]);
+          }
+        }
+      }
+
+      // ---- join the warps: the upper half into the lower half, then all threads over kBufs
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          st.l[c] += __shfl_xor_sync(0xffffffffu, st.l[c], o);
+          if constexpr (INT4) st.z[c] += __shfl_xor_sync(0xffffffffu, st.z[c], o);
+        }
+      }
+      float* mine = buf + (warp % kBufs) * C::kRegs * 32 + lane;
+      auto put = [&]() {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mine[i * 32] = st.acc[i >> 2][i & 3];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          mine[(32 + c) * 32] = st.m[c];
+          mine[(34 + c) * 32] = st.l[c];
+          if constexpr (INT4) mine[(36 + c) * 32] = st.z[c];
+        }
+      };
+      if (warp >= kBufs) put();
+      __syncthreads();
+      if (warp < kBufs) {
+        float fo[2], fm[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float mo = mine[(32 + c) * 32], m = fmaxf(mo, st.m[c]), r = ref_of(m);
+          fo[c] = exp2_fast(mo - r);
+          fm[c] = exp2_fast(st.m[c] - r);
+          st.m[c] = m;
+        }
+        scale_state(st, fm[0], fm[1]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          st.acc[i >> 2][i & 3] = fmaf(fo[i & 1], mine[i * 32], st.acc[i >> 2][i & 3]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          st.l[c] = fmaf(fo[c], mine[(34 + c) * 32], st.l[c]);
+          if constexpr (INT4) st.z[c] = fmaf(fo[c], mine[(36 + c) * 32], st.z[c]);
+        }
+        put();
+      }
+      __syncthreads();
+      const bool whole = g.gs >= f0 && g.ge <= f1;
+      const int group = g.b * a.hkv + g.kvh;
+      float* part = a.part + ((size_t)run * 2 + (g.gs < f0 ? 0 : 1)) * G * kPartStride;
+      for (int e = tid; e < G * kHeadDim; e += kWarps * 32) {
+        const int h = e / kHeadDim, d = e % kHeadDim;
+        int reg, ln;
+        if constexpr (INT4) {  // channel 16 g + 2 i + (row >= 8)
+          reg = ((d & 15) >> 1) * 4 + (d & 1) * 2 + (h & 1);
+          ln = (d >> 4) * 4 + (h >> 1);
+        } else {  // channel 16 i + row
+          reg = (d >> 4) * 4 + ((d >> 3) & 1) * 2 + (h & 1);
+          ln = (d & 7) * 4 + (h >> 1);
+        }
+        const int hl = h >> 1;  // the lane (g = 0) that holds the head's statistics
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kBufs; ++k)
+          m = fmaxf(m, buf[(k * C::kRegs + 32 + (h & 1)) * 32 + hl]);
+        const float r = ref_of(m);
+        float o = 0.f, l = 0.f, z = 0.f;
+#pragma unroll
+        for (int k = 0; k < kBufs; ++k) {
+          const float* bk = buf + k * C::kRegs * 32;
+          const float s = exp2_fast(bk[(32 + (h & 1)) * 32 + hl] - r);
+          float v = bk[reg * 32 + ln];
+          if constexpr (G < 8) v += bk[reg * 32 + ln + 2];
+          o = fmaf(s, v, o);
+          l = fmaf(s, bk[(34 + (h & 1)) * 32 + hl], l);
+          if constexpr (INT4) z = fmaf(s, bk[(36 + (h & 1)) * 32 + hl], z);
+        }
+        if constexpr (INT4) o = fmaf(o, 0x1p9f, z);
+        if (whole) {
+          const size_t row = (size_t)g.b * a.hq + g.kvh * G + h;
+          a.o[row * kHeadDim + d] = l == 0.f ? 0.f : o / l;
+          if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        } else {
+          part[h * kPartStride + d] = o;
+          if (d == 0) {
+            part[h * kPartStride + kHeadDim] = m;
+            part[h * kPartStride + kHeadDim + 1] = l;
+          }
+        }
+      }
+      if (!whole) {
+        // runs that hold tiles of the group: [first, last]
+        const int first = (int)(((long long)(g.gs + 1) * runs - 1) / total);
+        const int last = (int)(((long long)g.ge * runs - 1) / total);
+        __threadfence();
+        __syncthreads();
+        if (tid == 0)
+          is_last = atomicAdd(a.done + group, 1u) == (unsigned)(last - first);
+        __syncthreads();
+        if (is_last) {
+          __threadfence();
+          // Run `first` holds the group's start, so its partial is in its second slot; the others
+          // began inside the group: first slot.  buf becomes the parts' weights and then the
+          // columns of subsets of the parts, joined in a fixed order.
+          const int parts = last - first + 1;
+          auto at = [&](int c, int h) {
+            return a.part + (((size_t)(first + c) * 2 + (c == 0 ? 1 : 0)) * G + h) * kPartStride;
+          };
+          float* wt = buf;                    // [parts][G] maxima, then weights
+          float* ls = wt + parts * G;         // [parts][G] sums
+          for (int e = tid; e < parts * G; e += kWarps * 32) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(at(e / G, e % G) + kHeadDim));
+            wt[e] = ml.x;
+            ls[e] = ml.y;
+          }
+          __syncthreads();
+          constexpr int kSub = kWarps / G;    // warps per head
+          const int h = warp % G, sub = warp / G;
+          float m = -INFINITY;
+          for (int c = lane; c < parts; c += 32) m = fmaxf(m, wt[c * G + h]);
+          m = warp_max(m);
+          const float r = ref_of(m);
+          float l = 0.f;
+          for (int c = lane; c < parts; c += 32) l = fmaf(exp2_fast(wt[c * G + h] - r), ls[c * G + h], l);
+          l = warp_sum(l);
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int c = sub; c < parts; c += kSub) {
+            const float s = exp2_fast(wt[c * G + h] - r);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(at(c, h) + 4 * lane));
+            o.x = fmaf(s, v.x, o.x), o.y = fmaf(s, v.y, o.y);
+            o.z = fmaf(s, v.z, o.z), o.w = fmaf(s, v.w, o.w);
+          }
+          float4* cols = reinterpret_cast<float4*>(buf + (2 * parts * G + 3) / 4 * 4);
+          cols[warp * 32 + lane] = o;
+          __syncthreads();
+          if (sub == 0) {
+#pragma unroll
+            for (int k = 1; k < kSub; ++k) {
+              const float4 v = cols[(k * G + h) * 32 + lane];
+              o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            }
+            const size_t row = (size_t)g.b * a.hq + g.kvh * G + h;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            *reinterpret_cast<float4*>(a.o + row * kHeadDim + 4 * lane) =
+                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+            if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+          }
+          if (tid == 0) a.done[group] = 0u;
+        }
+      }
+      __syncthreads();  // buf is free again
+      gf = gend;
+    }
+    cp_async_wait_all();
+  }
+
+  if constexpr (INT4) {
+    // ---- the last CTA to leave advances the lengths: by then every CTA has read them
+    if (a.advance) {
+      __syncthreads();
+      if (tid == 0) {
+        __threadfence();
+        is_last = atomicAdd(a.left, 1u) == gridDim.x - 1;
+      }
+      __syncthreads();
+      if (is_last) {
+        for (int b = tid; b < a.batch; b += blockDim.x)
+          if (prefix[b + 1] != prefix[b]) a.seq_lens[b] += 1;
+        if (tid == 0) *a.left = 0u;
+      }
+    }
+  }
+}
+
+template <int G, bool INT4>
+cudaError_t launch_g(const Args& a, cudaStream_t s) {
+  const size_t smem = smem_bytes<INT4>(a.batch);
+  cudaError_t e = cudaFuncSetAttribute(k_window_decode<G, INT4>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  k_window_decode<G, INT4><<<num_sms(), Cfg<INT4>::kWarps * 32, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t workspace_bytes(int batch, int hq, int hkv) {
+  const size_t g = hq / hkv;
+  return (size_t)num_sms() * 2 * g * kPartStride * sizeof(float) +
+         ((size_t)batch * hkv + 1) * sizeof(unsigned);
+}
+
+void carve(Args& a, void* ws) {
+  const int g = a.hq / a.hkv;
+  a.part = static_cast<float*>(ws);
+  a.done = reinterpret_cast<unsigned*>(a.part + (size_t)num_sms() * 2 * g * kPartStride);
+  a.left = a.done + (size_t)a.batch * a.hkv;
+}
+
+cudaError_t launch(const Args& a, cudaStream_t s) {
+  const bool int4 = a.kc != nullptr;
+  switch (a.hq / a.hkv) {
+    case 1: return int4 ? launch_g<1, true>(a, s) : launch_g<1, false>(a, s);
+    case 2: return int4 ? launch_g<2, true>(a, s) : launch_g<2, false>(a, s);
+    case 4: return int4 ? launch_g<4, true>(a, s) : launch_g<4, false>(a, s);
+    case 8: return int4 ? launch_g<8, true>(a, s) : launch_g<8, false>(a, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace window
+}  // namespace twl

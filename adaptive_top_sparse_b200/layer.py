@@ -1,5 +1,8 @@
 """Device-side state of one decode-attention layer and the calls a user makes on it.
 
+``DecodeLayer`` is a layer with an fp16 cache, ``Int4Layer`` one whose cache is held in 4 bits, and
+``PageManager`` forks, frees, grows and compacts the pages either of them (or many) uses.
+
 ``DecodeLayer`` owns device tensors (PyTorch is only the allocator here): the paged fp16 K/V, the
 page table, the derived INT4 K and page bounds, a workspace, and the outputs.  Every computation
 is a call into libtwl.so.
@@ -34,6 +37,19 @@ def expect_tensor(name: str, t, shape, dtype, device) -> None:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensor is not contiguous")
+
+
+ALL_TOKENS = 2 ** 31 - 1        # a window of every token
+
+
+def on_device(device, call, *args) -> None:
+    """call(*args) with `device` current: a stream of None is then that device's current stream,
+    and the launch goes there whatever device the caller has current."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        call(*args)
+    else:
+        with torch.cuda.device(device):
+            call(*args)
 
 
 class DecodeLayer:
@@ -73,6 +89,12 @@ class DecodeLayer:
                                       max_pages=self.max_pages, max_budget=self.max_budget)
         self.o = torch.zeros((self.batch, num_q_heads, 128), dtype=torch.float32, device=dev)
         self.lse = torch.zeros((self.batch, num_q_heads), dtype=torch.float32, device=dev)
+        self.ws_window = twl.alloc_workspace(twl.TWL_OP_WINDOW_DECODE, dev, batch=self.batch,
+                                             num_q_heads=num_q_heads, num_kv_heads=num_kv_heads)
+        # made by the first window_prefill (not during a capture), or set to another layer's: layers
+        # of one shape whose calls run in order on one stream can share it
+        self.ws_prefill = None
+        self._pages = None
 
     @classmethod
     def from_workload(cls, wl, device="cuda"):
@@ -123,6 +145,50 @@ class DecodeLayer:
                             self.ws, stream)
         return self.o, self.lse
 
+    # ------------------------------------------------------------------ windowed attention
+    def window_decode(self, q, sinks: int = 0, window: int = ALL_TOKENS, stream=None):
+        """The last token of every sequence (already appended) attends to the first `sinks` tokens
+        and the last `window` ones: q [B][Hq][128] fp16 -> the layer's (o, lse)."""
+        self.expect_query(q)
+        on_device(self.k.device, twl.twl_window_decode, q, self.num_q_heads, self.kv, sinks,
+                  window, SM_SCALE, self.o, self.lse, self.ws_window, stream)
+        return self.o, self.lse
+
+    def window_prefill(self, q, q_start, sinks: int = 0, window: int = ALL_TOKENS, out=None,
+                       stream=None):
+        """Chunks of many tokens: rows q_start[b] .. q_start[b + 1] - 1 of q [T][Hq][128] fp16 are
+        the last tokens of sequence b (already in its cache) and attend causally under the window.
+        Returns (o fp16 [T][Hq][128], lse fp32 [T][Hq]), new tensors or the pair `out`; rows
+        outside every chunk are not written."""
+        dev = self.k.device
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q: expected a tensor [T][Hq][128]")
+        expect_tensor("q", q, (q.shape[0], self.num_q_heads, 128), torch.float16, dev)
+        expect_tensor("q_start", q_start, (self.batch + 1,), torch.int32, dev)
+        if out is None:
+            out = (torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device=dev))
+        o, lse = out
+        expect_tensor("o", o, q.shape, torch.float16, dev)
+        expect_tensor("lse", lse, q.shape[:2], torch.float32, dev)
+        if self.ws_prefill is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("window_prefill: the layer's first call makes its workspace, "
+                                   "so it cannot be captured")
+            self.ws_prefill = twl.alloc_workspace(
+                twl.TWL_OP_WINDOW_PREFILL, dev, batch=self.batch, num_q_heads=self.num_q_heads,
+                num_kv_heads=self.num_kv_heads)
+        on_device(dev, twl.twl_window_prefill, q, q_start, q.shape[0], self.num_q_heads, self.kv,
+                  sinks, window, SM_SCALE, o, lse, self.ws_prefill, stream)
+        return o, lse
+
+    # ------------------------------------------------------------------ pages
+    def pages(self) -> "PageManager":
+        """The page manager of this layer's cache and its derived K data (built on first use)."""
+        if self._pages is None:
+            self._pages = PageManager([self.k, self.v, self.aux.k_int4, self.aux.k_scale_zero,
+                                       self.aux.bounds], self.page_table, self.seq_lens)
+        return self._pages
+
     def expect_query(self, q) -> None:
         """q must be fp16 [B][Hq][128], contiguous, on the layer's GPU."""
         expect_tensor("q", q, (self.batch, self.num_q_heads, 128), torch.float16, self.k.device)
@@ -139,10 +205,150 @@ class DecodeLayer:
         return self._double_p
 
     def status(self, clear: bool = False):
-        return twl.twl_device_status(self.ws, clear)
+        """(status, flags) of the layer's device flags, over all of its workspaces."""
+        got = [twl.twl_device_status(ws, clear)
+               for ws in (self.ws, self.ws_window, self.ws_prefill) if ws is not None]
+        return next((st for st, _ in got if st != twl.TWL_OK), twl.TWL_OK), \
+            got[0][1] | got[1][1] | (got[2][1] if len(got) > 2 else 0)
 
 
 SM_SCALE = 1.0 / math.sqrt(128.0)
+
+
+class Int4Layer:
+    """One layer whose paged cache is held in 4 bits, and attention over it.
+
+    k, v: uint8 codes [num_phys_pages][num_kv_heads][16][64]; k_sz, v_sz: fp16 scale and zero of
+    every row [..][16][2]; page_table, seq_lens as DecodeLayer.  All are device tensors that the
+    layer uses in place.  Issue the calls on a layer in order on one stream: they share its
+    workspace."""
+
+    def __init__(self, k, k_sz, v, v_sz, page_table, seq_lens, num_q_heads: int,
+                 num_kv_heads: int):
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k: expected a tensor [P][Hkv][16][64]")
+        dev, p_phys = k.device, k.shape[0]
+        for name, t in (("k", k), ("v", v)):
+            expect_tensor(name, t, (p_phys, num_kv_heads, 16, 64), torch.uint8, dev)
+        for name, t in (("k_sz", k_sz), ("v_sz", v_sz)):
+            expect_tensor(name, t, (p_phys, num_kv_heads, 16, 2), torch.float16, dev)
+        expect_table(page_table, seq_lens, dev)
+        self.k, self.k_sz, self.v, self.v_sz = k, k_sz, v, v_sz
+        self.page_table, self.seq_lens = page_table, seq_lens
+        self.num_q_heads, self.num_kv_heads = num_q_heads, num_kv_heads
+        self.device = dev
+        self.kv = twl.Int4KV(k, k_sz, v, v_sz, page_table, seq_lens, num_kv_heads, p_phys)
+        self.batch = self.kv.batch
+        self.ws = twl.alloc_workspace(twl.TWL_OP_INT4_DECODE, dev, batch=self.batch,
+                                      num_q_heads=num_q_heads, num_kv_heads=num_kv_heads)
+        self.o = torch.zeros((self.batch, num_q_heads, 128), dtype=torch.float32, device=dev)
+        self.lse = torch.zeros((self.batch, num_q_heads), dtype=torch.float32, device=dev)
+        self._pages = None
+
+    @classmethod
+    def from_fp16(cls, k, v, page_table, seq_lens, num_q_heads: int, num_kv_heads: int,
+                  stream=None):
+        """The layer of an fp16 cache (device tensors, layout of DecodeLayer): quantises K and V
+        of every page the sequences use."""
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k: expected a tensor [P][Hkv][16][128]")
+        dev, p_phys = k.device, k.shape[0]
+        for name, t in (("k", k), ("v", v)):
+            expect_tensor(name, t, (p_phys, num_kv_heads, 16, 128), torch.float16, dev)
+        expect_table(page_table, seq_lens, dev)
+        made = []
+        for x in (k, v):
+            codes = torch.zeros((p_phys, num_kv_heads, 16, 64), dtype=torch.uint8, device=dev)
+            sz = torch.zeros((p_phys, num_kv_heads, 16, 2), dtype=torch.float16, device=dev)
+            on_device(dev, twl.twl_quantize_k, twl.PagedKV(x, x, page_table, seq_lens,
+                                                           num_kv_heads, p_phys),
+                      codes, sz, None, stream)
+            made += [codes, sz]
+        return cls(*made, page_table, seq_lens, num_q_heads, num_kv_heads)
+
+    def decode(self, q, k_new=None, v_new=None, sinks: int = 0, window: int = ALL_TOKENS,
+               advance: bool = True, stream=None):
+        """Appends the token (k_new, v_new) [B][Hkv][128] fp16 of every sequence in 4 bits (its
+        page must be mapped) and attends from it, in one launch: q [B][Hq][128] fp16 -> the
+        layer's (o, lse).  With advance, seq_lens moves on.  Without k_new and v_new the last
+        cached token attends and nothing is written."""
+        dev = self.device
+        expect_tensor("q", q, (self.batch, self.num_q_heads, 128), torch.float16, dev)
+        if (k_new is None) != (v_new is None):
+            raise ValueError("k_new and v_new go together")
+        if k_new is not None:
+            for name, t in (("k_new", k_new), ("v_new", v_new)):
+                expect_tensor(name, t, (self.batch, self.num_kv_heads, 128), torch.float16, dev)
+        on_device(dev, twl.twl_int4_decode, q, self.num_q_heads, self.kv, k_new, v_new,
+                  advance and k_new is not None, sinks, window, SM_SCALE, self.o, self.lse,
+                  self.ws, stream)
+        return self.o, self.lse
+
+    def pages(self) -> "PageManager":
+        """The page manager of this layer's cache (built on first use)."""
+        if self._pages is None:
+            self._pages = PageManager([self.k, self.k_sz, self.v, self.v_sz], self.page_table,
+                                      self.seq_lens)
+        return self._pages
+
+    def status(self, clear: bool = False):
+        return twl.twl_device_status(self.ws, clear)
+
+
+def expect_table(page_table, seq_lens, device) -> None:
+    """page_table int32 [B][max_pages] and seq_lens int32 [B], contiguous, on `device`."""
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table: expected a tensor [B][max_pages]")
+    expect_tensor("page_table", page_table, page_table.shape, torch.int32, device)
+    expect_tensor("seq_lens", seq_lens, page_table.shape[:1], torch.int32, device)
+
+
+class PageManager:
+    """The pages of one page table and of every pool (tensor [num_phys_pages][...]) it indexes:
+    the K and V of one layer, or of all layers that share the table.  Uses the tensors in place.
+    A page is in use when the table names it; nothing else is kept.  Issue the calls in order on
+    one stream, the one that the attention calls on the same cache use."""
+
+    def __init__(self, pools, page_table, seq_lens):
+        pools = list(pools)
+        if not pools or not all(isinstance(t, torch.Tensor) and t.dim() >= 1 for t in pools):
+            raise ValueError("pools: expected tensors [num_phys_pages][...]")
+        dev, p_phys = pools[0].device, pools[0].shape[0]
+        for t in pools:
+            expect_tensor("pool", t, (p_phys, *t.shape[1:]), t.dtype, dev)
+        expect_table(page_table, seq_lens, dev)
+        self.pools, self.page_table, self.seq_lens = pools, page_table, seq_lens
+        self.device, self.num_phys_pages = dev, p_phys
+        self.batch, self.max_pages = page_table.shape
+        self.ws = twl.alloc_workspace(twl.TWL_OP_PAGES, dev, batch=self.batch,
+                                      max_pages=self.max_pages, rows=p_phys)
+        self.num_used = torch.zeros((), dtype=torch.int32, device=dev)
+
+    def remap(self, parent, reserve=None, sinks: int = 0, window: int = ALL_TOKENS,
+              stream=None) -> None:
+        """One page-table step: slot b goes on as parent[b]'s sequence (itself, a fork of another
+        slot, or -1: freed) with pages for reserve[b] more tokens; pages that no later query sees
+        under (sinks, window) are dropped.  parent, reserve: int32 [B] device tensors.  A step
+        that cannot be carried out changes nothing and shows in status()."""
+        expect_tensor("parent", parent, (self.batch,), torch.int32, self.device)
+        if reserve is not None:
+            expect_tensor("reserve", reserve, (self.batch,), torch.int32, self.device)
+        on_device(self.device, twl.twl_remap_pages, self.pools, self.page_table, self.seq_lens,
+                  self.num_phys_pages, parent, reserve, sinks, window, self.ws, stream)
+
+    def compact(self, table_out=None, stream=None):
+        """Moves the used pages to the front of the pools.  The table with the new numbers goes to
+        table_out, or replaces the page table.  Returns the manager's device scalar with the
+        number of used pages."""
+        if table_out is None:
+            table_out = self.page_table
+        expect_tensor("table_out", table_out, self.page_table.shape, torch.int32, self.device)
+        on_device(self.device, twl.twl_compact_pages, self.pools, self.page_table, table_out,
+                  self.num_phys_pages, self.num_used, self.ws, stream)
+        return self.num_used
+
+    def status(self, clear: bool = False):
+        return twl.twl_device_status(self.ws, clear)
 
 
 class DoubleP:

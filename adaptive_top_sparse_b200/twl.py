@@ -28,8 +28,10 @@ TWL_ERR_TIMEOUT = -4
 TWL_ERR_WORKSPACE = -5
 TWL_ERR_BAD_INDEX = -6
 TWL_ERR_SCRATCH_LIMIT = -7
+TWL_ERR_NO_PAGES = -8
 TWL_FLAG_BAD_INDEX = 1
 TWL_FLAG_TIMEOUT = 2
+TWL_FLAG_NO_PAGES = 4
 
 TWL_OP_CACHE = 1
 TWL_OP_SELECT = 2
@@ -39,13 +41,20 @@ TWL_OP_UNION = 5
 TWL_OP_SPARSE_DECODE = 6
 TWL_OP_DECODE_STEP = 7
 TWL_OP_SELECT_CLUSTERS = 8
+TWL_OP_WINDOW_DECODE = 9
+TWL_OP_WINDOW_PREFILL = 10
+TWL_OP_INT4_DECODE = 11
+TWL_OP_PAGES = 12
+
+TWL_MAX_POOLS = 128
 
 EXPORTED = [
     "twl_workspace_bytes", "twl_workspace_init", "twl_device_status", "twl_status_string",
     "twl_page_bounds", "twl_quantize_k", "twl_append_token", "twl_quantize_k_nbit",
     "twl_estimate_nbit", "twl_page_centroids", "twl_select_clusters_top_p", "twl_select_pages", "twl_estimate", "twl_prune_top_p",
     "twl_group_union", "twl_sparse_decode", "twl_decode_step", "twl_noalloc_scratch_bytes",
-    "twl_sparse_decode_noalloc", "twl_test_set_waits",
+    "twl_sparse_decode_noalloc", "twl_window_decode", "twl_window_prefill", "twl_int4_decode",
+    "twl_remap_pages", "twl_compact_pages", "twl_test_set_waits",
 ]
 
 
@@ -70,6 +79,18 @@ class _StepStats(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("sel_pages", "sel_count", "weights", "cand_tok",
                                           "cand_count", "threshold", "kept_count", "union_tok",
                                           "union_count")]
+
+
+class _Int4KV(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("k_scale_zero", C.c_void_p), ("v", C.c_void_p),
+                ("v_scale_zero", C.c_void_p), ("page_table", C.c_void_p),
+                ("seq_lens", C.c_void_p), ("batch", C.c_int32), ("num_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("page_size", C.c_int32), ("max_pages", C.c_int32),
+                ("num_phys_pages", C.c_int32)]
+
+
+class _PagePool(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("page_bytes", C.c_int64)]
 
 
 _vp, _i32, _f32, _sz = C.c_void_p, C.c_int32, C.c_float, C.c_size_t
@@ -104,6 +125,16 @@ _sigs = {
     "twl_decode_step": (_i32, [_vp, _i32, C.POINTER(_PagedKV), C.POINTER(_KAux), _i32, _i32,
                                _i32, _f32, _f32, _vp, _vp, C.POINTER(_StepStats), _vp, _sz,
                                _vp]),
+    "twl_window_decode": (_i32, [_vp, _i32, C.POINTER(_PagedKV), _i32, _i32, _f32, _vp, _vp, _vp,
+                                 _sz, _vp]),
+    "twl_window_prefill": (_i32, [_vp, _vp, _i32, _i32, C.POINTER(_PagedKV), _i32, _i32, _f32,
+                                  _vp, _vp, _vp, _sz, _vp]),
+    "twl_int4_decode": (_i32, [_vp, _i32, C.POINTER(_Int4KV), _vp, _vp, _i32, _i32, _i32, _f32,
+                               _vp, _vp, _vp, _sz, _vp]),
+    "twl_remap_pages": (_i32, [C.POINTER(_PagePool), _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp,
+                               _i32, _i32, _vp, _sz, _vp]),
+    "twl_compact_pages": (_i32, [C.POINTER(_PagePool), _i32, _vp, _vp, _i32, _i32, _i32, _vp,
+                                 _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _sigs.items():
     _fn = getattr(_lib, _name)
@@ -337,3 +368,77 @@ def twl_sparse_decode_noalloc(q, num_q_heads: int, kv: PagedKV, tok, tok_count, 
                                           _ptr(tok_count), tok_stride, sm_scale, _ptr(o),
                                           _ptr(lse), _stream(stream)),
            "twl_sparse_decode_noalloc")
+
+
+def twl_window_decode(q, num_q_heads: int, kv: PagedKV, sinks: int, window: int, sm_scale: float,
+                      o, lse, ws=None, stream=None) -> None:
+    ckv = kv.c()
+    _check(_lib.twl_window_decode(_ptr(q), num_q_heads, C.byref(ckv), sinks, window, sm_scale,
+                                  _ptr(o), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)),
+           "twl_window_decode")
+
+
+def twl_window_prefill(q, q_start, total_q: int, num_q_heads: int, kv: PagedKV, sinks: int,
+                       window: int, sm_scale: float, o, lse, ws=None, stream=None) -> None:
+    ckv = kv.c()
+    _check(_lib.twl_window_prefill(_ptr(q), _ptr(q_start), total_q, num_q_heads, C.byref(ckv),
+                                   sinks, window, sm_scale, _ptr(o), _ptr(lse), _ptr(ws),
+                                   _nbytes(ws), _stream(stream)), "twl_window_prefill")
+
+
+@dataclass
+class Int4KV:
+    """Tensors of a paged cache held in 4 bits (see include/twl.h for the layout)."""
+    k: torch.Tensor
+    k_scale_zero: torch.Tensor
+    v: torch.Tensor
+    v_scale_zero: torch.Tensor
+    page_table: torch.Tensor
+    seq_lens: torch.Tensor
+    num_kv_heads: int
+    num_phys_pages: int
+    head_dim: int = 128
+    page_size: int = 16
+
+    @property
+    def batch(self) -> int:
+        return int(self.page_table.shape[0])
+
+    @property
+    def max_pages(self) -> int:
+        return int(self.page_table.shape[1])
+
+    def c(self) -> _Int4KV:
+        return _Int4KV(_ptr(self.k), _ptr(self.k_scale_zero), _ptr(self.v),
+                       _ptr(self.v_scale_zero), _ptr(self.page_table), _ptr(self.seq_lens),
+                       self.batch, self.num_kv_heads, self.head_dim, self.page_size,
+                       self.max_pages, self.num_phys_pages)
+
+
+def twl_int4_decode(q, num_q_heads: int, kv: Int4KV, k_new, v_new, advance: bool, sinks: int,
+                    window: int, sm_scale: float, o, lse, ws=None, stream=None) -> None:
+    ckv = kv.c()
+    _check(_lib.twl_int4_decode(_ptr(q), num_q_heads, C.byref(ckv), _ptr(k_new), _ptr(v_new),
+                                1 if advance else 0, sinks, window, sm_scale, _ptr(o), _ptr(lse),
+                                _ptr(ws), _nbytes(ws), _stream(stream)), "twl_int4_decode")
+
+
+def _pools(pools):
+    """The pools (tensors [P][...]) as an array of twl_page_pool."""
+    return (_PagePool * len(pools))(*[(_ptr(t), _nbytes(t) // t.shape[0]) for t in pools])
+
+
+def twl_remap_pages(pools, page_table, seq_lens, num_phys_pages: int, parent, reserve, sinks: int,
+                    window: int, ws=None, stream=None) -> None:
+    _check(_lib.twl_remap_pages(_pools(pools), len(pools), _ptr(page_table), _ptr(seq_lens),
+                                page_table.shape[0], page_table.shape[1], num_phys_pages,
+                                _ptr(parent), _ptr(reserve), sinks, window, _ptr(ws),
+                                _nbytes(ws), _stream(stream)), "twl_remap_pages")
+
+
+def twl_compact_pages(pools, page_table, page_table_out, num_phys_pages: int, num_used, ws=None,
+                      stream=None) -> None:
+    _check(_lib.twl_compact_pages(_pools(pools), len(pools), _ptr(page_table),
+                                  _ptr(page_table_out), page_table.shape[0], page_table.shape[1],
+                                  num_phys_pages, _ptr(num_used), _ptr(ws), _nbytes(ws),
+                                  _stream(stream)), "twl_compact_pages")

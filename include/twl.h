@@ -39,7 +39,8 @@
  *   k, v          fp16  [num_phys_pages][num_kv_heads][page_size][head_dim]
  *   page_table    int32 [batch][max_pages]   logical page j of sequence b -> physical page;
  *                                            entries j >= ceil(seq_lens[b] / 16) are ignored
- *   seq_lens      int32 [batch]              tokens of each sequence (>= 1)
+ *   seq_lens      int32 [batch]              tokens of each sequence (>= 1; a call that also takes
+ *                                            an empty slot, length 0, says so)
  * Derived K data, same physical paging ([Summary] B.1, 4.3):
  *   k_int4        uint8 [num_phys_pages][num_kv_heads][16][64]   channel 2j in the low nibble of
  *                                                                byte j of its token row
@@ -66,10 +67,12 @@ typedef int32_t twl_status;
 #define TWL_ERR_WORKSPACE (-5)   /* workspace NULL, misaligned or smaller than required */
 #define TWL_ERR_BAD_INDEX (-6)   /* device flag: page table / seq_lens / index list out of range */
 #define TWL_ERR_SCRATCH_LIMIT (-7) /* request larger than twl_sparse_decode_noalloc's scratch */
+#define TWL_ERR_NO_PAGES (-8)    /* device flag: twl_remap_pages wants more pages than are free */
 
 /* Device flag bits reported by twl_device_status (sticky until cleared). */
 #define TWL_FLAG_BAD_INDEX 1u
 #define TWL_FLAG_TIMEOUT 2u
+#define TWL_FLAG_NO_PAGES 4u
 
 typedef void* twl_stream_t; /* a cudaStream_t */
 
@@ -117,6 +120,10 @@ typedef struct twl_step_stats {
 #define TWL_OP_SPARSE_DECODE 6 /* twl_sparse_decode (row_stride = tok_stride) */
 #define TWL_OP_DECODE_STEP 7   /* twl_decode_step                           */
 #define TWL_OP_SELECT_CLUSTERS 8 /* twl_select_clusters_top_p                 */
+#define TWL_OP_WINDOW_DECODE 9 /* twl_window_decode                         */
+#define TWL_OP_WINDOW_PREFILL 10 /* twl_window_prefill                        */
+#define TWL_OP_INT4_DECODE 11  /* twl_int4_decode                           */
+#define TWL_OP_PAGES 12        /* twl_remap_pages, twl_compact_pages (rows = num_phys_pages) */
 size_t twl_workspace_bytes(int32_t op, int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                            int32_t max_pages, int32_t max_budget, int32_t rows,
                            int32_t row_stride);
@@ -127,7 +134,8 @@ size_t twl_workspace_bytes(int32_t op, int32_t batch, int32_t num_q_heads, int32
 twl_status twl_workspace_init(void* ws, size_t ws_bytes, twl_stream_t stream);
 
 /* Wait for `stream`, then report the sticky device flags of `ws` in *flags (may be NULL).
- * Returns TWL_OK if no flag is set, else TWL_ERR_BAD_INDEX or TWL_ERR_TIMEOUT.  If clear != 0
+ * Returns TWL_OK if no flag is set, else TWL_ERR_BAD_INDEX, TWL_ERR_TIMEOUT or
+ * TWL_ERR_NO_PAGES.  If clear != 0
  * the flags are reset to zero afterwards. */
 twl_status twl_device_status(void* ws, uint32_t* flags, int32_t clear, twl_stream_t stream);
 
@@ -319,6 +327,125 @@ twl_status twl_sparse_decode_noalloc(const void* q, int32_t num_q_heads, const t
                                      const int32_t* tok, const int32_t* tok_count,
                                      int32_t tok_stride, float sm_scale, float* o, float* lse,
                                      twl_stream_t stream);
+
+/* ---------------------------------------------------------------- windowed attention
+ * Dense attention over the paged cache under a sliding window with sinks (the window keeps the
+ * cost of a token constant; the first tokens of a sequence, which attract weight whatever they
+ * hold, stay visible): the query at position t of its sequence sees key j iff
+ *   j <= t  and  (j < sinks or j > t - window).
+ * sinks >= 0, window >= 1; window = INT32_MAX sees every token.  o = softmax(sm_scale q K^T) V
+ * over the seen keys (fp16 K/V, fp32 sums), lse = natural-log sum of exp of the scaled scores.
+ * Only pages that hold a seen key are read: the table may have -1 for the others.  K and V rows
+ * nobody sees may hold anything (NaN included).  sm_scale must be positive and finite.
+ *
+ * twl_window_decode: one token per sequence, the last one (t = seq_lens[b] - 1; it is in the
+ *   cache already, see twl_append_token).
+ *   q float16 [B][Hq][128]; o float [B][Hq][128] out; lse float [B][Hq] out
+ *   A sequence of length 0 is an empty slot: o = 0, lse = -inf, no flag.  A page that is out of
+ *   range is skipped and a length < 0 or > 16 * max_pages is an empty slot, both with
+ *   TWL_FLAG_BAD_INDEX.  Workspace TWL_OP_WINDOW_DECODE (batch, num_q_heads, num_kv_heads),
+ *   zeroed once by twl_workspace_init; every launch leaves its counters zero for the next.
+ *   batch * num_kv_heads <= 4096 (TWL_ERR_UNSUPPORTED above).
+ * twl_window_prefill: the last q_len_b tokens of every sequence, q_len_b = q_start[b + 1] -
+ *   q_start[b] (a prompt, a chunk of one, or drafted tokens to verify).  Row q_start[b] + i of q
+ *   sits at position seq_lens[b] - q_len_b + i; its K and V are in the cache already.
+ *   q float16 [total_q][Hq][128]; q_start int32 [B + 1], ascending from >= 0 to <= total_q
+ *   o float16 [total_q][Hq][128] out; lse float [total_q][Hq] out
+ *   Rows of q outside every chunk are not read and their outputs not written.  q_len_b = 0 is
+ *   fine.  A sequence whose chunk is not inside [0, total_q] or longer than its length, or whose
+ *   length is > 16 * max_pages, is skipped (its outputs are not written), and a page that is out
+ *   of range is skipped, both with TWL_FLAG_BAD_INDEX.  total_q = 0 launches nothing.
+ *   Workspace TWL_OP_WINDOW_PREFILL (batch, num_q_heads, num_kv_heads), zeroed once. */
+twl_status twl_window_decode(const void* q, int32_t num_q_heads, const twl_paged_kv* kv,
+                             int32_t sinks, int32_t window, float sm_scale, float* o, float* lse,
+                             void* ws, size_t ws_bytes, twl_stream_t stream);
+twl_status twl_window_prefill(const void* q, const int32_t* q_start, int32_t total_q,
+                              int32_t num_q_heads, const twl_paged_kv* kv, int32_t sinks,
+                              int32_t window, float sm_scale, void* o, float* lse, void* ws,
+                              size_t ws_bytes, twl_stream_t stream);
+
+/* ---------------------------------------------------------------- a cache held in 4 bits
+ * K and V as 4-bit codes with an fp16 scale and zero per token row (the scheme and layout of
+ * twl_quantize_k, which fills either from an fp16 cache: pass V as kv->k): 136 instead of 512
+ * bytes per token and kv-head, and no fp16 copy.
+ * twl_int4_decode: with k_new and v_new (fp16 [B][Hkv][128]), the new token of every sequence is
+ *   quantised and written to position n_b = seq_lens[b], which the caller has mapped, and query b
+ *   at t = n_b attends over the n_b + 1 tokens, the new one's quantised row among them, under the
+ *   window and sinks of twl_window_decode; with both NULL nothing is written and t = n_b - 1.
+ *   Scores and sums are those of the rows x = code * scale + zero.  If advance != 0 (with k_new
+ *   only), seq_lens[b] becomes n_b + 1 behind the last read, in the same launch.
+ *   q, o, lse as twl_window_decode.  An empty slot (n_b = 0, and with k_new an unmapped first
+ *   page, table entry -1) gives o = 0, lse = -inf and is left alone; a position that has no
+ *   mapped page and a bad length do the same and raise TWL_FLAG_BAD_INDEX.  Two sequences must
+ *   not append to one physical page (fork with twl_remap_pages).
+ *   Workspace TWL_OP_INT4_DECODE (batch, num_q_heads, num_kv_heads), zeroed once.
+ *   batch * num_kv_heads <= 4096 (TWL_ERR_UNSUPPORTED above). */
+typedef struct twl_int4_kv {
+  void* k;                    /* uint8 [P][Hkv][16][64]  codes, as k_int4 above */
+  void* k_scale_zero;         /* fp16  [P][Hkv][16][2]   (scale, zero)          */
+  void* v;                    /* as k                                           */
+  void* v_scale_zero;
+  const int32_t* page_table;  /* int32 [batch][max_pages]                       */
+  int32_t* seq_lens;          /* int32 [batch]; written with advance            */
+  int32_t batch;
+  int32_t num_kv_heads;
+  int32_t head_dim;           /* must be 128 */
+  int32_t page_size;          /* must be 16  */
+  int32_t max_pages;
+  int32_t num_phys_pages;
+} twl_int4_kv;
+twl_status twl_int4_decode(const void* q, int32_t num_q_heads, const twl_int4_kv* kv,
+                           const void* k_new, const void* v_new, int32_t advance, int32_t sinks,
+                           int32_t window, float sm_scale, float* o, float* lse, void* ws,
+                           size_t ws_bytes, twl_stream_t stream);
+
+/* ---------------------------------------------------------------- pages of a cache
+ * A pool is any array [num_phys_pages][page_bytes] that the page table indexes (K, V, codes,
+ * bounds; of one layer or of many).  page_bytes is a multiple of 16, data 16-byte aligned.
+ * Which pages are in use is what the table says: nothing else is kept.  Every non-negative entry
+ * is a use; a negative one is none.
+ *
+ * twl_remap_pages: one page-table step.  parent int32 [B]: slot b continues parent[b]'s sequence
+ *   (itself: goes on; another slot: a fork; -1: the slot is freed).  reserve int32 [B] (or NULL:
+ *   none): tokens for which slot b needs pages behind its length (a freed slot's are the pages of
+ *   the next sequence in it).  With n = the parent's length (0 for -1), in logical pages j of 16
+ *   tokens:
+ *   - whole pages of the n tokens are shared with the parent, except those that no query from
+ *     position n on sees under (sinks, window): they are dropped (-1);
+ *   - a last page that is partly filled is shared by nobody: it stays with the parent's own slot
+ *     if that continues itself, else with its lowest fork; every other fork gets a copy of it,
+ *     in every pool, in a new page;
+ *   - pages j < ceil((n + reserve[b]) / 16) behind that are kept if slot b goes on itself and has
+ *     them, else new;
+ *   - every other entry becomes -1, seq_lens[b] becomes n (0 for a freed slot).
+ *   New pages are the lowest ones that the new table does not hold, in (slot, j) order.  Pages
+ *   out of use need no call to be freed.  The call is carried out whole or not at all: an entry
+ *   >= num_phys_pages that a slot would hold, a parent outside [-1, B), a bad length, a negative
+ *   reserve or one that does not fit max_pages raise TWL_FLAG_BAD_INDEX, and too few free pages
+ *   raise TWL_FLAG_NO_PAGES; then nothing is changed.
+ * twl_compact_pages: moves the used pages of highest number into the free ones of lowest, so that
+ *   the used pages become 0 .. *num_used - 1 (a pool can then shrink, or be saved as a prefix):
+ *   the i-th used page at or above *num_used goes to the i-th free page below it, in every pool.
+ *   page_table_out (may be page_table) gets the table with the new numbers.  An entry
+ *   >= num_phys_pages raises TWL_FLAG_BAD_INDEX and nothing is changed.
+ * Both: page_table int32 [batch][max_pages], seq_lens int32 [batch], 1 <= num_pools <=
+ *   TWL_MAX_POOLS, workspace TWL_OP_PAGES (batch, max_pages, rows = num_phys_pages), zeroed once;
+ *   batch > 4096 or num_phys_pages > 8388608 (2^23): TWL_ERR_UNSUPPORTED.  One cooperative launch each
+ *   (every SM takes one CTA); a wait that gives up raises TWL_FLAG_TIMEOUT (state undefined). */
+#define TWL_MAX_POOLS 128
+typedef struct twl_page_pool {
+  void* data;
+  int64_t page_bytes;
+} twl_page_pool;
+twl_status twl_remap_pages(const twl_page_pool* pools, int32_t num_pools, int32_t* page_table,
+                           int32_t* seq_lens, int32_t batch, int32_t max_pages,
+                           int32_t num_phys_pages, const int32_t* parent, const int32_t* reserve,
+                           int32_t sinks, int32_t window, void* ws, size_t ws_bytes,
+                           twl_stream_t stream);
+twl_status twl_compact_pages(const twl_page_pool* pools, int32_t num_pools,
+                             const int32_t* page_table, int32_t* page_table_out, int32_t batch,
+                             int32_t max_pages, int32_t num_phys_pages, int32_t* num_used,
+                             void* ws, size_t ws_bytes, twl_stream_t stream);
 
 /* ---------------------------------------------------------------- the whole step
  * select -> estimate -> prune (p, eps) -> group union -> attend, with sm_scale = 1/sqrt(128)
