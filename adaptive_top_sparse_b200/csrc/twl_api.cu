@@ -228,7 +228,7 @@ size_t twl_workspace_bytes(int32_t op, int32_t batch, int32_t num_q_heads, int32
       break;
     case TWL_OP_WINDOW_PREFILL:
       if (num_kv_heads < 1 || num_q_heads < num_kv_heads) return 0;
-      c.take<char>(prefill::workspace_bytes(batch, num_q_heads, num_kv_heads));
+      c.take<char>(prefill::workspace_bytes());
       break;
     case TWL_OP_PAGES:
       if (rows < 0) return 0;
@@ -601,12 +601,14 @@ twl_status twl_window_prefill(const void* q, const int32_t* q_start, int32_t tot
   if (st != TWL_OK) return st;
   if ((st = check_heads(num_q_heads, k.hkv)) != TWL_OK) return st;
   if ((st = check_window(sinks, window, sm_scale)) != TWL_OK) return st;
+  // a row of 128 values of the cache is a coordinate of the copies: 31 bits
+  if ((uint64_t)k.num_phys * (uint64_t)k.hkv * kPage > 0x7FFFFFFFull) return TWL_ERR_UNSUPPORTED;
   if (total_q < 0 || !q_start || !aligned(q_start, 4)) return TWL_ERR_INVALID_ARG;
   if (total_q > 0 && (!q || !o || !lse || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4)))
     return TWL_ERR_INVALID_ARG;
   if ((long long)k.batch * k.hkv > 4096) return TWL_ERR_UNSUPPORTED;
   Carve c{static_cast<char*>(ws)};
-  void* body = c.take<char>(prefill::workspace_bytes(k.batch, num_q_heads, k.hkv));
+  void* body = c.take<char>(prefill::workspace_bytes());
   if ((st = check_ws(ws, ws_bytes, c.off)) != TWL_OK) return st;
   if (total_q == 0) return TWL_OK;
   prefill::Args a = {};

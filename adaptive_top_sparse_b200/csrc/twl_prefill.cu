@@ -5,8 +5,28 @@
 // (j < sinks or j > t - window).  o = softmax(scale q K^T) V over the seen keys in one pass: the
 // running maximum and sum of each row rescale the accumulator when the maximum grows.
 //
-// Work split: the G heads of a kv-head share its keys, so the rows of a unit are (query, head)
-// pairs, 64 per CTA; keys come in tiles of 64 tokens (4 pages).
+// Units: the G heads of a kv-head share its keys, so a row is a (query, head) pair and a unit is
+// 256 rows (256 / G queries) of one (sequence, kv-head): two query tiles of 128 rows that share
+// every key tile of 128 tokens (8 pages).  The key tiles of all units form one flat list that is
+// cut into equal runs, one per CTA (one CTA per SM); a unit cut by runs leaves fp32 partials that
+// the CTA arriving last merges in run order.  So a few long sequences with a handful of queries
+// use the card as well as one long prompt, and lengths stay on the device.
+//
+// One CTA: eleven warps.
+//   loader     TMA of the queries and of K and V pages (16 rows of 128 bytes a copy, 128-byte
+//              swizzle) into a ring of five 32 KB buffers
+//   fixer      zeroes the V rows nobody in the unit sees (a weight of 0 times a stale infinity
+//              would be NaN); only tiles at the edge of what is seen need it
+//   mma        one thread: S_x = Q_x K^T (tcgen05, fp16 in, fp32 in TMEM) and O_x += P_x V with P
+//              in TMEM over S and V taken as it lies in the page (MN-major)
+//   softmax x  four warps per query tile, a thread per row: scores from TMEM, maximum, weights
+//              back to TMEM as fp16, sums in fp32.  While one tile's softmax runs, the tensor core
+//              works for the other.
+// The weights enter the product as fp16 (2^-11 of each, as the fp16 result itself); maxima, sums
+// and accumulators are fp32.  Waits are bounded: one that gives up raises TWL_FLAG_TIMEOUT and
+// the CTA leaves without its outputs.
+#include <cuda.h>
+
 #include "twl_common.cuh"
 #include "twl_kernels.h"
 #include "twl_prefill.h"
@@ -16,197 +36,790 @@ namespace prefill {
 namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kRows = 64, kKeys = 64, kThreads = 128;
+constexpr float kSlack = 8.f;  // log2: a row's maximum is raised only when exceeded by more
+constexpr int kRows = 256, kTileRows = 128, kKeys = 128;
+constexpr int kThreads = 352;
+constexpr int kBufBytes = 32768, kBufs = 5;
+constexpr int kQBytes = 65536;
+constexpr int kRecs = 8;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
+// partial of a cut unit: o as [32][256] float4 (column group, row), then max[256], sum[256]
+constexpr int kPartFloats = kRows * 130;
 
+struct Smem {
+  // barriers
+  uint64_t q_full, q_free;
+  uint64_t full[kBufs], empty[kBufs];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t v_ready[kBufs];  // V of the buffer is loaded and its unseen rows are zero
+  uint32_t tmem;
+  int aborted;
+  int rec[kRecs];  // pages of a key tile that were loaded (bit per page)
+  int is_last;
+  // where the run starts
+  int b, kvh, qt, tile;
+  int red[32];
+};
+constexpr size_t kSmemBytes = 1024 + kQBytes + (size_t)kBufs * kBufBytes + sizeof(Smem);
+
+// ------------------------------------------------------------------ PTX
 __device__ __forceinline__ uint32_t sptr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+__device__ __forceinline__ void bar_init(uint64_t* b, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sptr(b)), "r"(count) : "memory");
 }
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(sptr(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(sptr(b)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.b32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(sptr(b)), "r"(parity), "r"(20000u) : "memory");
+  return ok != 0;
+}
+constexpr uint32_t kWaitLimit = 1u << 16;  // polls of up to 20 us each
+
+// Waits for the phase of the given parity; false when the wait, or another in the CTA, gave up.
+__device__ __forceinline__ bool bar_wait(Smem& s, uint64_t* b, uint32_t parity, uint32_t* flags) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (bar_try(b, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&s.aborted)) return false;
+  }
+  *reinterpret_cast<volatile int*>(&s.aborted) = 1;
+  raise_flag(flags, TWL_FLAG_TIMEOUT);
+  return false;
+}
+// The same for a converged warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool warp_wait(Smem& s, uint64_t* b, uint32_t parity, uint32_t* flags) {
+  return __all_sync(0xffffffffu, bar_wait(s, b, parity, flags));
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Queries of sequence b's chunk, or 0 (and a flag) when its lengths cannot be served.
-__device__ int chunk_len(const Args& a, int b, bool report) {
-  const int s = a.q_start[b], e = a.q_start[b + 1], n = a.seq_lens[b];
-  if (s < 0 || e < s || e > a.total_q || n < e - s || n > a.max_pages * kPage) {
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                       uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(sptr(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                       uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(sptr(bar))
+      : "memory");
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle: lead and stride are the distances in bytes
+// between 64-element blocks of the contiguous dimension (MN-major only) and between groups of 8
+// rows of the other one.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 |
+         (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// Instruction descriptor: fp16 x fp16 -> fp32, M = 128, N = 128; B as K-major or MN-major.
+constexpr uint32_t kIdescQK = 1u << 4 | (128u / 8) << 17 | (128u / 16) << 24;
+constexpr uint32_t kIdescPV = kIdescQK | 1u << 16;
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b),
+      "r"(kIdescQK), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b),
+      "r"(kIdescPV), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sptr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+#define TWL_R8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), \
+                     "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+#define TWL_O8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
+                     "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define TWL_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), \
+                     "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+// 32 columns of the warp's 32 lanes: register c of lane l = column c of TMEM lane l.  The values
+// are there after wait_ld (keep_ld ties them to it).
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : TWL_O8(r, 0), TWL_O8(r, 8), TWL_O8(r, 16), TWL_O8(r, 24) : "r"(addr));
+}
+__device__ __forceinline__ void keep_ld(uint32_t (&r)[32]) {
+  asm volatile("" : TWL_R8(r, 0), TWL_R8(r, 8), TWL_R8(r, 16), TWL_R8(r, 24));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];" : TWL_O8(r, 0), TWL_O8(r, 8) : "r"(addr));
+}
+__device__ __forceinline__ void keep_ld16(uint32_t (&r)[16]) {
+  asm volatile("" : TWL_R8(r, 0), TWL_R8(r, 8));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(addr), TWL_I8(r, 0), TWL_I8(r, 8) : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+// ------------------------------------------------------------------ the flat list
+struct Chunk {
+  int qs, qn, n;  // first row of q, queries, cached length
+};
+
+// Sequence b's chunk; qn = 0 (and a flag, by `report`) when it cannot be served.
+__device__ __forceinline__ Chunk chunk_of(const Args& a, int b, bool report) {
+  Chunk c;
+  c.qs = a.q_start[b];
+  const int e = a.q_start[b + 1];
+  c.n = a.seq_lens[b];
+  c.qn = e - c.qs;
+  if (c.qs < 0 || e < c.qs || e > a.total_q || c.n < c.qn || c.n > a.max_pages * kPage) {
     if (report) raise_flag(a.flags, TWL_FLAG_BAD_INDEX);
-    return 0;
+    c.qn = 0;
   }
-  return e - s;
+  return c;
+}
+
+// The keys of a unit of queries [i0, i0 + queries) of a chunk.
+struct Span {
+  int t0, t1;              // positions of its first and last query
+  int lo;                  // first key of any of its windows
+  int sink_tiles, first;   // tiles of the sinks; first tile behind them
+  int tiles;
+};
+__device__ __forceinline__ Span span_of(const Args& a, const Chunk& c, int i0, int queries) {
+  Span s;
+  s.t0 = c.n - c.qn + i0;
+  s.t1 = min(s.t0 + queries, c.n) - 1;
+  s.lo = s.t0 >= a.window ? s.t0 - a.window + 1 : 0;
+  s.first = s.lo / kKeys;
+  s.sink_tiles = min((min(a.sinks, c.n) + kKeys - 1) / kKeys, s.first);
+  s.tiles = s.sink_tiles + s.t1 / kKeys - s.first + 1;
+  return s;
+}
+
+// Every role walks the CTA's run of the list by itself: segments of units, in order.
+template <int G>
+struct Walk {
+  static constexpr int kQueries = kRows / G;
+  const Args& a;
+  long long at, end;     // place in the flat list
+  int b, kvh, qt, tile;  // of the next segment
+  Chunk c;
+  // the current segment
+  Span s;
+  int i0, tile0, tiles;  // first query, first key tile, key tiles
+  bool whole, two;       // the whole unit; it has rows in the second query tile
+
+  __device__ Walk(const Args& a, const Smem& sm, long long f0, long long f1)
+      : a(a), at(f0), end(f1), b(sm.b), kvh(sm.kvh), qt(sm.qt), tile(sm.tile) {
+    if (at < end) c = chunk_of(a, b, false);
+  }
+  __device__ bool next() {
+    if (at >= end) return false;
+    while (qt * kQueries >= c.qn) {
+      qt = 0;
+      if (++kvh >= a.hkv || c.qn == 0) {
+        kvh = 0;
+        c = chunk_of(a, ++b, false);
+      }
+    }
+    i0 = qt * kQueries;
+    s = span_of(a, c, i0, kQueries);
+    tile0 = tile;
+    tiles = (int)min((long long)(s.tiles - tile), end - at);
+    whole = tiles == s.tiles;
+    two = i0 + kTileRows / G < c.qn;
+    at += tiles;
+    tile += tiles;
+    if (tile == s.tiles) tile = 0, ++qt;
+    return true;
+  }
+  // First token of the segment's key tile i.
+  __device__ int base_of(int i) const {
+    const int x = tile0 + i;
+    return (x < s.sink_tiles ? x : s.first + x - s.sink_tiles) * kKeys;
+  }
+  // Whether the tile at `base` holds keys that no query of the unit sees.
+  __device__ bool ragged(int base, int pages) const {
+    return pages != 0xFF || base + kKeys - 1 > s.t1 || (base < s.lo && base + kKeys > a.sinks);
+  }
+};
+
+template <int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_window_prefill(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap qmap,
+                     const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* base_ptr = reinterpret_cast<unsigned char*>(
+      ((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  unsigned char* qbuf = base_ptr;
+  unsigned char* ring = base_ptr + kQBytes;
+  Smem& sm = *reinterpret_cast<Smem*>(ring + (size_t)kBufs * kBufBytes);
+  long long* prefix = reinterpret_cast<long long*>(ring);  // [batch + 1], before the first load
+  constexpr int kQueries = kRows / G;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // ---- prefix[b] = key tiles per kv-head of the sequences before b
+  for (int b = warp; b < a.batch; b += kThreads / 32) {
+    const Chunk c = chunk_of(a, b, blockIdx.x == 0 && lane == 0);
+    long long sum = 0;
+    for (int i = lane * kQueries; i < c.qn; i += 32 * kQueries)
+      sum += span_of(a, c, i, kQueries).tiles;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) prefix[b + 1] = sum;
+  }
+  if (tid == 0) prefix[0] = 0;
+  __syncthreads();
+  if (warp == 0) {
+    long long carry = 0;
+    for (int b0 = 1; b0 <= a.batch; b0 += 32) {
+      long long x = b0 + lane <= a.batch ? prefix[b0 + lane] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      x += carry;
+      if (b0 + lane <= a.batch) prefix[b0 + lane] = x;
+      carry = __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+  const long long total = prefix[a.batch] * a.hkv;
+  const int runs = (int)min((long long)gridDim.x, total);
+  const int run = blockIdx.x;
+  if (run >= runs) return;
+  const long long f0 = total * run / runs, f1 = total * (run + 1) / runs;
+  if (warp == 0) {
+    int x = 0, y = a.batch;  // prefix[x] hkv <= f0 < prefix[y] hkv
+    while (y - x > 1) {
+      const int mid = (x + y) >> 1;
+      if (prefix[mid] * a.hkv <= f0) x = mid;
+      else y = mid;
+    }
+    const long long per = prefix[x + 1] - prefix[x], in = f0 - prefix[x] * a.hkv;
+    long long rest = in % per;
+    const Chunk c = chunk_of(a, x, false);
+    for (int q0 = 0;; q0 += 32) {  // the unit that holds tile `rest` of this kv-head
+      const int i = (q0 + lane) * kQueries;
+      const int t = i < c.qn ? span_of(a, c, i, kQueries).tiles : 0;
+      int sum = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, rest < sum);
+      if (hit) {
+        if (lane == __ffs(hit) - 1) {
+          sm.b = x;
+          sm.kvh = (int)(in / per);
+          sm.qt = q0 + lane;
+          sm.tile = (int)(rest - (sum - t));
+        }
+        break;
+      }
+      rest -= __shfl_sync(0xffffffffu, sum, 31);
+      if (q0 * kQueries >= c.qn) break;  // not reached: rest is below the sum of all units
+    }
+  }
+  if (tid == 0) {
+    sm.aborted = 0;
+    bar_init(&sm.q_full, 1);
+    bar_init(&sm.q_free, 1);
+    for (int i = 0; i < kBufs; ++i) bar_init(&sm.full[i], 1), bar_init(&sm.empty[i], 2);
+    for (int x = 0; x < 2; ++x) {
+      bar_init(&sm.s_full[x], 1);
+      bar_init(&sm.p_full[x], 4);
+      bar_init(&sm.o_full[x], 1);
+      bar_init(&sm.o_free[x], 4);
+    }
+    for (int i = 0; i < kBufs; ++i) bar_init(&sm.v_ready[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     sptr(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  // the prefix lay where TMA writes next
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sm.tmem;
+  Walk<G> w(a, sm, f0, f1);
+  auto dead = [&]() { return *reinterpret_cast<volatile int*>(&sm.aborted) != 0; };
+
+  if (warp == kLoadWarp) {
+    // ================================================================ loader
+    int fill = 0, ntile = 0, nseg = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      if (nseg > 0) ok = warp_wait(sm, &sm.q_free, (nseg - 1) & 1, a.flags);
+      ++nseg;
+      if (!ok) break;
+      if (lane == 0) {
+        bar_expect(&sm.q_full, w.two ? kQBytes : kQBytes / 2);
+        for (int x = 0; x < (w.two ? 2 : 1); ++x)
+          for (int h = 0; h < 2; ++h)
+            tma_3d(sptr(qbuf) + x * 32768 + h * 16384, &qmap, 64 * h, w.kvh * G,
+                   w.c.qs + w.i0 + x * (kTileRows / G), &sm.q_full);
+      }
+      for (int i = 0; i < w.tiles; ++i, ++ntile) {
+        const int base = w.base_of(i);
+        int phys = -1;
+        if (lane < kKeys / kPage) {
+          const int p0 = base + lane * kPage;
+          if (p0 <= w.s.t1 && (p0 < a.sinks || p0 + kPage > w.s.lo))
+            phys = load_phys(a.page_table, w.b, p0 / kPage, a.max_pages, a.num_phys, a.flags);
+        }
+        const unsigned pages = __ballot_sync(0xffffffffu, phys >= 0);
+        const int row = (__shfl_sync(0xffffffffu, phys, (lane & 15) >> 1) * a.hkv + w.kvh) * kPage;
+        const bool mine = pages >> ((lane & 15) >> 1) & 1;
+        for (int kv = 0; kv < 2; ++kv, ++fill) {
+          const int buf = fill % kBufs, round = fill / kBufs;
+          if (round > 0 && !warp_wait(sm, &sm.empty[buf], (round - 1) & 1, a.flags)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            if (kv == 0) sm.rec[ntile % kRecs] = (int)pages;
+            bar_expect(&sm.full[buf], __popc(pages) * 4096);
+          }
+          __syncwarp();
+          if (lane < 16 && mine)
+            tma_2d(sptr(ring) + buf * kBufBytes + (lane & 1) * 16384 + (lane >> 1) * 2048,
+                   kv == 0 ? &kmap : &vmap, 64 * (lane & 1), row, &sm.full[buf]);
+        }
+        if (!ok) break;
+      }
+    }
+    // an aborted CTA leaves only behind its copies in flight
+    if (!ok || dead()) {
+      const long long t0 = clock64();
+      for (int k = max(0, fill - kBufs); k < fill; ++k)
+        while (!bar_try(&sm.full[k % kBufs], (k / kBufs) & 1) && clock64() - t0 < 2000000000ll) {
+        }
+      if (nseg > 0)
+        while (!bar_try(&sm.q_full, (nseg - 1) & 1) && clock64() - t0 < 2000000000ll) {
+        }
+    }
+  } else if (warp == kMmaWarp) {
+    // ================================================================ tensor core
+    if (lane == 0) {
+      int kfill = 0, nseg = 0;
+      uint32_t pph[2] = {0, 0};
+      int units[2] = {0, 0};
+      bool ok = true;
+      auto scores = [&](int x, uint32_t kaddr) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+          mma_ss(tmem + x * 128, smem_desc(sptr(qbuf) + x * 32768 + off, 16, 1024),
+                 smem_desc(kaddr + off, 16, 1024), k > 0);
+        }
+        mma_commit(&sm.s_full[x]);
+      };
+      auto wait_fill = [&](int f) {
+        return bar_wait(sm, &sm.full[f % kBufs], (f / kBufs) & 1, a.flags);
+      };
+      auto addr_of = [&](int f) { return sptr(ring) + (f % kBufs) * kBufBytes; };
+      while (ok && w.next()) {
+        const int xs = w.two ? 2 : 1;
+        ok = bar_wait(sm, &sm.q_full, nseg & 1, a.flags) && wait_fill(kfill);
+        ++nseg;
+        if (!ok) break;
+        fence_after();
+        for (int x = 0; x < xs; ++x) scores(x, addr_of(kfill));
+        mma_commit(&sm.empty[kfill % kBufs]);
+        if (w.tiles == 1) mma_commit(&sm.q_free);
+        for (int i = 0; i < w.tiles && ok; ++i, kfill += 2) {
+          const int vf = kfill + 1;
+          for (int x = 0; x < xs; ++x) {
+            ok = bar_wait(sm, &sm.p_full[x], pph[x], a.flags);
+            pph[x] ^= 1;
+            if (ok && i == 0 && units[x] > 0)
+              ok = bar_wait(sm, &sm.o_free[x], (units[x] - 1) & 1, a.flags);
+            if (ok && x == 0) {
+              // a buffer takes K and V in turn: its n-th V is fill (2 n + const) kBufs + buffer
+              ok = bar_wait(sm, &sm.v_ready[vf % kBufs], (vf / (2 * kBufs)) & 1, a.flags);
+            }
+            if (!ok) break;
+            fence_after();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8,
+                     smem_desc(addr_of(vf) + k * 2048, 16384, 1024), i > 0 || k > 0);
+            if (i + 1 == w.tiles) {
+              mma_commit(&sm.o_full[x]);
+              ++units[x];
+            } else {
+              if (x == 0) ok = wait_fill(kfill + 2);
+              if (!ok) break;
+              scores(x, addr_of(kfill + 2));
+            }
+          }
+          if (!ok) break;
+          mma_commit(&sm.empty[vf % kBufs]);
+          if (i + 1 < w.tiles) mma_commit(&sm.empty[(kfill + 2) % kBufs]);
+          if (i + 2 == w.tiles) mma_commit(&sm.q_free);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kFixWarp) {
+    // ================================================================ fixer
+    int fill = 0, ntile = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      for (int i = 0; i < w.tiles && ok; ++i, ++ntile) {
+        for (int kv = 0; kv < 2; ++kv, ++fill) {
+          const int buf = fill % kBufs;
+          ok = warp_wait(sm, &sm.full[buf], (fill / kBufs) & 1, a.flags);
+          if (!ok) break;
+          const int base = w.base_of(i), pages = sm.rec[ntile % kRecs];
+          if (kv == 1 && w.ragged(base, pages)) {
+            for (int r = lane; r < kKeys; r += 32) {
+              const int key = base + r;
+              const bool seen = key <= w.s.t1 && (key < a.sinks || key >= w.s.lo) &&
+                                (pages >> (r / kPage) & 1);
+              if (!seen) {
+                unsigned char* p = ring + buf * kBufBytes + r * 128;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  const int cc = ((c + lane) & 7) * 16;
+                  *reinterpret_cast<uint4*>(p + cc) = make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4*>(p + 16384 + cc) = make_uint4(0, 0, 0, 0);
+                }
+              }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          __syncwarp();
+          if (lane == 0) {
+            if (kv == 1) bar_arrive(&sm.v_ready[buf]);
+            bar_arrive(&sm.empty[buf]);
+          }
+        }
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    // ================================================================ softmax of query tile x
+    const int x = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * 128;
+    uint32_t sph = 0, oph = 0;
+    int ntile = 0;
+    while (w.next()) {
+      const int i = w.i0 + (x * kTileRows + row) / G;  // the row's query
+      const int t = w.c.n - w.c.qn + i;
+      const bool active = x == 0 || w.two;
+      const bool valid = i < w.c.qn;
+      float m = -INFINITY, l = 0.f;
+      // first and last query of this tile of rows: tiles of keys that all of them see need no mask
+      const int ta = w.s.t0 + x * (kTileRows / G), tb = min(ta + kTileRows / G, w.c.n) - 1;
+      for (int j = 0; active && j < w.tiles; ++j) {
+        if (!warp_wait(sm, &sm.s_full[x], sph, a.flags)) break;
+        sph ^= 1;
+        fence_after();
+        const int base = w.base_of(j), pages = sm.rec[(ntile + j) % kRecs];
+        const bool clear = pages == 0xFF && base + kKeys - 1 <= ta &&
+                           (base > tb - a.window || base + kKeys <= a.sinks);
+        const int hi = t - base, lo = max(t - a.window, -1) - base, sk = a.sinks - base;
+        auto mask = [&](uint32_t (&v)[32], int c) {
+          if (clear) return;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const int col = 32 * c + k;
+            const bool see = col <= hi && (col > lo || col < sk) && (pages >> (col / kPage) & 1);
+            v[k] = see ? v[k] : 0xFF800000u;
+          }
+        };
+        // The row is read from TMEM twice, 32 columns at a time and one load ahead: for its maximum
+        // and for its weights (128 registers to keep it in would leave too few for the rest).
+        uint32_t v0[32], v1[32];
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto maxima = [&](uint32_t (&v)[32], int c) {
+          mask(v, c);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(v[k]));
+        };
+        tmem_ld32(v0, ts);
+        wait_ld();
+        keep_ld(v0);
+        tmem_ld32(v1, ts + 32);
+        maxima(v0, 0);
+        wait_ld();
+        keep_ld(v1);
+        tmem_ld32(v0, ts + 64);
+        maxima(v1, 1);
+        wait_ld();
+        keep_ld(v0);
+        tmem_ld32(v1, ts + 96);
+        maxima(v0, 2);
+        wait_ld();
+        keep_ld(v1);
+        tmem_ld32(v0, ts);
+        maxima(v1, 3);
+        wait_ld();
+        keep_ld(v0);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        if (__any_sync(0xffffffffu, top > m + kSlack)) {
+          const float mn = fmaxf(m, top);
+          const float f = exp2_fast(m - ref_of(mn));
+          m = mn;
+          l *= f;
+          if (j > 0) {  // this tile's scores were issued behind the last product into O
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_ld16(o, to + 16 * c);
+              wait_ld();
+              keep_ld16(o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st16(to + 16 * c, o);
+            }
+          }
+        }
+        const float ref = ref_of(m);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // P's columns 16 c .. of chunk c lie over scores that have been read by then
+        auto weights = [&](uint32_t (&v)[32], int c) {
+          mask(v, c);
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float p0 = exp2_fast(fmaf(__uint_as_float(v[k]), a.scale_log2, -ref));
+            const float p1 = exp2_fast(fmaf(__uint_as_float(v[k + 1]), a.scale_log2, -ref));
+            sum[k & 2] += p0;
+            sum[(k & 2) + 1] += p1;
+            const __half2 h = __floats2half2_rn(p0, p1);
+            p[k >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          tmem_st16(ts + 16 * c, p);
+        };
+        tmem_ld32(v1, ts + 32);
+        wait_ld();
+        keep_ld(v1);
+        weights(v0, 0);
+        tmem_ld32(v0, ts + 64);
+        weights(v1, 1);
+        wait_ld();
+        keep_ld(v0);
+        tmem_ld32(v1, ts + 96);
+        weights(v0, 2);
+        wait_ld();
+        keep_ld(v1);
+        weights(v1, 3);
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sm.p_full[x]);
+      }
+      ntile += w.tiles;
+      // ---- the unit's rows
+      if (active && warp_wait(sm, &sm.o_full[x], oph, a.flags)) fence_after();
+      if (active) oph ^= 1;
+      const bool fine = !__any_sync(0xffffffffu, dead());
+      const size_t out = (size_t)(w.c.qs + i) * a.hq + w.kvh * G + row % G;
+      float* part = a.part + ((size_t)run * 2 + (w.tile0 > 0 ? 0 : 1)) * kPartFloats;
+      const int prow = x * kTileRows + row;
+      if (active && fine) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o, to + 32 * c);
+          wait_ld();
+          keep_ld(o);
+          if (valid && w.whole) {
+            uint32_t h[16];
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const __half2 v = __floats2half2_rn(__uint_as_float(o[k]) * inv,
+                                                  __uint_as_float(o[k + 1]) * inv);
+              h[k >> 1] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(a.o + out * kHeadDim + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[k] = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+          } else if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(part);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              dst[(8 * c + k) * kRows + prow] =
+                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+          __syncwarp();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sm.o_free[x]);
+        if (valid && w.whole)
+          a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (valid && !w.whole) {
+          part[kRows * kHeadDim + prow] = m;
+          part[kRows * (kHeadDim + 1) + prow] = l;
+        }
+      }
+      if (w.whole) continue;
+      // ---- a cut unit: the run that arrives last merges the partials, in run order
+      const long long fs = w.at - w.tiles - w.tile0;  // the unit's first tile in the list
+      const int first = (int)(((fs + 1) * runs - 1) / total);
+      const int last = (int)(((fs + w.s.tiles) * runs - 1) / total);
+      __threadfence();
+      named_sync(1, 256);
+      if (tid == 0)
+        sm.is_last = !dead() && atomicAdd(a.done + first, 1u) == (unsigned)(last - first);
+      named_sync(1, 256);
+      if (sm.is_last) {
+        __threadfence();
+        const int rows = min(kRows, (w.c.qn - w.i0) * G);
+        auto at = [&](int r) {  // the unit starts in run `first`: its second slot
+          return a.part + ((size_t)r * 2 + (r == first ? 1 : 0)) * kPartFloats;
+        };
+        for (int e = tid; e < rows * 32; e += 256) {
+          const int r = e % rows, c = e / rows;
+          float mm = -INFINITY;
+          for (int k = first; k <= last; ++k) mm = fmaxf(mm, __ldcg(at(k) + kRows * kHeadDim + r));
+          const float ref = ref_of(mm);
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          float ll = 0.f;
+#pragma unroll 4
+          for (int k = first; k <= last; ++k) {
+            const float* p = at(k);
+            const float f = exp2_fast(__ldcg(p + kRows * kHeadDim + r) - ref);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + c * kRows + r);
+            ll = fmaf(f, __ldcg(p + kRows * (kHeadDim + 1) + r), ll);
+            o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
+            o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+          }
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;
+          const size_t dst = (size_t)(w.c.qs + w.i0 + r / G) * a.hq + w.kvh * G + r % G;
+          *reinterpret_cast<uint2*>(a.o + dst * kHeadDim + 4 * c) =
+              make_uint2(pack_half2(__float2half_rn(o.x * inv), __float2half_rn(o.y * inv)),
+                         pack_half2(__float2half_rn(o.z * inv), __float2half_rn(o.w * inv)));
+          if (c == 0) a.lse[dst] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+        }
+        if (tid == 0) a.done[first] = 0u;
+      }
+      named_sync(1, 256);
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// Rows of 128 fp16 values in boxes of 64 columns (one 128-byte swizzle row).
+bool encode(CUtensorMap* map, const uint16_t* base, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<uint16_t*>(base), dims,
+                     strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int G>
-__global__ void __launch_bounds__(kThreads) k_window_prefill(const __grid_constant__ Args a) {
-  constexpr int kQueries = kRows / G;
-  __shared__ __align__(128) unsigned char ks[kKeys * 256], vs[kKeys * 256];
-  __shared__ int scan_sh[33], s_b, s_unit, s_phys[kKeys / kPage];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, lg = lane >> 2, lt = lane & 3;
-
-  // the unit: (sequence, 64 / G queries, kv-head)
-  const int kvh = blockIdx.x % a.hkv, unit = blockIdx.x / a.hkv;
-  if (tid == 0) s_b = -1;
-  int carry = 0;
-  for (int base = 0; base < a.batch; base += kThreads) {
-    const int b = base + tid;
-    const int c = b < a.batch ? (chunk_len(a, b, blockIdx.x == 0) + kQueries - 1) / kQueries : 0;
-    int total;
-    const int ex = carry + block_exclusive_scan(c, scan_sh, &total);
-    if (unit >= ex && unit < ex + c) s_b = b, s_unit = unit - ex;
-    carry += total;
-  }
-  __syncthreads();
-  if (s_b < 0) return;
-  const int b = s_b, i0 = s_unit * kQueries;
-  const int qs = a.q_start[b], qn = a.q_start[b + 1] - qs, n = a.seq_lens[b];
-  const int t0 = n - qn + i0, t1 = min(t0 + kQueries, n) - 1;  // positions of the unit's queries
-  const int lo = t0 >= a.window ? t0 - a.window + 1 : 0;       // first key of any window
-
-  uint32_t qa[8][4];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int row = warp * 16 + lg + 8 * r;
-    const int i = i0 + row / G;
-    const uint16_t* src = a.q + ((size_t)(qs + i) * a.hq + kvh * G + row % G) * kHeadDim + 2 * lt;
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      qa[kk][r] = i < qn ? *reinterpret_cast<const uint32_t*>(src + 16 * kk) : 0u;
-      qa[kk][2 + r] = i < qn ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8) : 0u;
-    }
-  }
-  float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
-
-  const int first = lo / kKeys, last = t1 / kKeys;
-  const int sink_tiles = min((min(a.sinks, n) + kKeys - 1) / kKeys, first);
-  for (int x = 0; x < sink_tiles + last - first + 1; ++x) {
-    const int base = (x < sink_tiles ? x : first + x - sink_tiles) * kKeys;
-    __syncthreads();
-    if (tid < kKeys / kPage) {
-      // a page is read when some query sees one of its keys
-      const int p0 = base + tid * kPage;
-      int ph = -1;
-      if (p0 <= t1 && (p0 < a.sinks || p0 + kPage > lo))
-        ph = load_phys(a.page_table, b, p0 / kPage, a.max_pages, a.num_phys, a.flags);
-      s_phys[tid] = ph;
-    }
-    __syncthreads();
-    for (int it = 0; it < kKeys * 16 / kThreads; ++it) {
-      const int r = it * (kThreads / 16) + (tid >> 4), c = tid & 15, tok = base + r;
-      const int ph = s_phys[r / kPage];
-      const bool ok = ph >= 0 && tok <= t1 && (tok < a.sinks || tok >= lo);
-      const size_t off = ok ? (((size_t)ph * a.hkv + kvh) * kPage + (r & 15)) * kHeadDim + c * 8 : 0;
-      const int slot = r * 256 + ((c ^ (r & 7)) * 16);
-      cp_async16(ks + slot, a.k + off, ok);
-      cp_async16(vs + slot, a.v + off, ok);
-    }
-    cp_async_commit();
-    cp_async_wait_all();
-    __syncthreads();
-    float s[8][4];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s[j][c] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const int r = 8 * j + (lane >> 4) * 8 + (lane & 7);
-        uint32_t f[4];
-        ldmatrix4(f, sptr(ks) + r * 256 + (((2 * kk + ((lane >> 3) & 1)) ^ (r & 7)) * 16));
-        mma_16816(s[j], qa[kk], f[0], f[1]);
-        mma_16816(s[j + 1], qa[kk], f[2], f[3]);
-      }
-    }
-    float mt[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int key = base + 8 * j + 2 * lt + (c & 1);
-        const int t = t0 + (warp * 16 + lg + 8 * (c >> 1)) / G;
-        const bool see = key <= t && (key < a.sinks || key > t - a.window) && t < n &&
-                         s_phys[(8 * j) / kPage] >= 0;
-        s[j][c] = see ? s[j][c] * a.scale_log2 : -INFINITY;
-        mt[c >> 1] = fmaxf(mt[c >> 1], s[j][c]);
-      }
-    float ref[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 1));
-      mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 2));
-      mt[r] = fmaxf(mt[r], m[r]);
-      ref[r] = mt[r] == -INFINITY ? 0.f : mt[r];
-      const float f = exp2f(m[r] - ref[r]);
-      m[r] = mt[r];
-      l[r] *= f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[i][2 * r] *= f, o[i][2 * r + 1] *= f;
-    }
-    uint32_t p[4][4];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        s[j][c] = exp2f(s[j][c] - ref[c >> 1]);
-        l[c >> 1] += s[j][c];
-      }
-      p[j >> 1][(j & 1) * 2] = pack_half2(__float2half_rn(s[j][0]), __float2half_rn(s[j][1]));
-      p[j >> 1][(j & 1) * 2 + 1] = pack_half2(__float2half_rn(s[j][2]), __float2half_rn(s[j][3]));
-    }
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const int r = 16 * kk + (lane & 15);
-        uint32_t f[4];
-        ldmatrix4_trans(f, sptr(vs) + r * 256 + (((i + (lane >> 4)) ^ (r & 7)) * 16));
-        mma_16816(o[i], p[kk], f[0], f[1]);
-        mma_16816(o[i + 1], p[kk], f[2], f[3]);
-      }
-  }
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    const int row = warp * 16 + lg + 8 * r, i = i0 + row / G;
-    if (i >= qn) continue;
-    const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
-    const size_t out = (size_t)(qs + i) * a.hq + kvh * G + row % G;
-#pragma unroll
-    for (int c = 0; c < 16; ++c)
-      *reinterpret_cast<uint32_t*>(a.o + out * kHeadDim + 8 * c + 2 * lt) =
-          pack_half2(__float2half_rn(o[c][2 * r] * inv), __float2half_rn(o[c][2 * r + 1] * inv));
-    if (lt == 0) a.lse[out] = l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
-  }
+cudaError_t launch_g(const Args& a, cudaStream_t s) {
+  CUtensorMap qm, km, vm;
+  const cuuint64_t qd[3] = {kHeadDim, (cuuint64_t)a.hq, (cuuint64_t)a.total_q};
+  const cuuint64_t qst[2] = {kHeadDim * 2, (cuuint64_t)a.hq * kHeadDim * 2};
+  const cuuint32_t qbox[3] = {64, G, kTileRows / G};
+  const cuuint64_t kd[2] = {kHeadDim, (cuuint64_t)a.num_phys * a.hkv * kPage};
+  const cuuint64_t kst[1] = {kHeadDim * 2};
+  const cuuint32_t kbox[2] = {64, kPage};
+  if (!encode_fn() || !encode(&qm, a.q, 3, qd, qst, qbox) || !encode(&km, a.k, 2, kd, kst, kbox) ||
+      !encode(&vm, a.v, 2, kd, kst, kbox))
+    return cudaErrorNotSupported;
+  cudaError_t e = cudaFuncSetAttribute(k_window_prefill<G>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  k_window_prefill<G><<<num_sms(), kThreads, kSmemBytes, s>>>(a, qm, km, vm);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t workspace_bytes(int batch, int hq, int hkv) { return 0; }
+size_t workspace_bytes() {
+  return (size_t)num_sms() * (2 * kPartFloats * sizeof(float) + sizeof(unsigned));
+}
 
-cudaError_t launch(const Args& a, void* ws, cudaStream_t s) {
-  const int g = a.hq / a.hkv;
-  const long long blocks =
-      ((long long)a.total_q * g / kRows + a.batch) * a.hkv;  // at least the units of any split
-#define TWL_PRE(G) k_window_prefill<G><<<(unsigned)blocks, kThreads, 0, s>>>(a)
-  switch (g) {
-    case 1: TWL_PRE(1); break;
-    case 2: TWL_PRE(2); break;
-    case 4: TWL_PRE(4); break;
-    case 8: TWL_PRE(8); break;
+cudaError_t launch(Args a, void* ws, cudaStream_t s) {
+  a.part = static_cast<float*>(ws);
+  a.done = reinterpret_cast<unsigned*>(a.part + (size_t)num_sms() * 2 * kPartFloats);
+  switch (a.hq / a.hkv) {
+    case 1: return launch_g<1>(a, s);
+    case 2: return launch_g<2>(a, s);
+    case 4: return launch_g<4>(a, s);
+    case 8: return launch_g<8>(a, s);
     default: return cudaErrorInvalidValue;
   }
-#undef TWL_PRE
-  return cudaGetLastError();
 }
 
 }  // namespace prefill

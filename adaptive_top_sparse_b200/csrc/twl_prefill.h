@@ -21,10 +21,13 @@ struct Args {
   uint16_t* o;       // [total_q][hq][128]
   float* lse;        // [total_q][hq]
   uint32_t* flags;
+  // workspace, set by launch()
+  float* part;     // [SMs][2][256 rows x 130] partials of units cut by runs
+  unsigned* done;  // [SMs] arrived partials, by the run the unit starts in; zero between launches
 };
 
-size_t workspace_bytes(int batch, int hq, int hkv);
-cudaError_t launch(const Args& a, void* ws, cudaStream_t s);
+size_t workspace_bytes();
+cudaError_t launch(Args a, void* ws, cudaStream_t s);
 
 }  // namespace prefill
 }  // namespace twl
