@@ -196,6 +196,40 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Two fp32 values in one register pair.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t y;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+  return y;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t y;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+  return y;
+}
+// The lowest n of 32 bits (none for n <= 0).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+// Which of the columns c .. c + 31 of a key tile a row sees: column <= hi and (column > lo or
+// column < sk), on pages that were loaded.
+__device__ __forceinline__ uint32_t seen_bits(int c, int hi, int lo, int sk, int pages) {
+  const uint32_t on = (pages >> (c / kPage) & 1 ? 0x0000FFFFu : 0u) |
+                      (pages >> (c / kPage + 1) & 1 ? 0xFFFF0000u : 0u);
+  return low_bits(hi - c + 1) & (~low_bits(lo - c + 1) | low_bits(sk - c)) & on;
+}
+__device__ __forceinline__ void hide(uint32_t (&v)[32], uint32_t seen) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = seen >> k & 1u ? v[k] : 0xFF800000u;
+}
 __device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f : m; }
 
 // ------------------------------------------------------------------ the flat list
@@ -567,44 +601,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool clear = pages == 0xFF && base + kKeys - 1 <= ta &&
                            (base > tb - a.window || base + kKeys <= a.sinks);
         const int hi = t - base, lo = max(t - a.window, -1) - base, sk = a.sinks - base;
-        auto mask = [&](uint32_t (&v)[32], int c) {
-          if (clear) return;
+        // A row goes through the loops 32 columns at a time, twice (for its maximum, then for its
+        // weights): TMEM answers in some 20 cycles, and loops this short stay in the instruction
+        // cache (unrolled over the row, half of the softmax warps' time went to fetching them).
+        uint32_t v[32];
+        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < kKeys; c += 32) {
+          tmem_ld32(v, ts + c);
+          wait_ld();
+          keep_ld(v);
+          if (!clear) hide(v, seen_bits(c, hi, lo, sk, pages));
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int col = 32 * c + k;
-            const bool see = col <= hi && (col > lo || col < sk) && (pages >> (col / kPage) & 1);
-            v[k] = see ? v[k] : 0xFF800000u;
+          for (int k = 0; k < 32; k += 4) {
+            m0 = max3(m0, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+            m1 = max3(m1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
           }
-        };
-        // The row is read from TMEM twice, 32 columns at a time and one load ahead: for its maximum
-        // and for its weights (128 registers to keep it in would leave too few for the rest).
-        uint32_t v0[32], v1[32];
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto maxima = [&](uint32_t (&v)[32], int c) {
-          mask(v, c);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(v[k]));
-        };
-        tmem_ld32(v0, ts);
-        wait_ld();
-        keep_ld(v0);
-        tmem_ld32(v1, ts + 32);
-        maxima(v0, 0);
-        wait_ld();
-        keep_ld(v1);
-        tmem_ld32(v0, ts + 64);
-        maxima(v1, 1);
-        wait_ld();
-        keep_ld(v0);
-        tmem_ld32(v1, ts + 96);
-        maxima(v0, 2);
-        wait_ld();
-        keep_ld(v1);
-        tmem_ld32(v0, ts);
-        maxima(v1, 3);
-        wait_ld();
-        keep_ld(v0);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        }
+        const float top = fmaxf(m0, m1) * a.scale_log2;
         if (__any_sync(0xffffffffu, top > m + kSlack)) {
           const float mn = fmaxf(m, top);
           const float f = exp2_fast(m - ref_of(mn));
@@ -624,36 +638,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float ref = ref_of(m);
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        // P's columns 16 c .. of chunk c lie over scores that have been read by then
-        auto weights = [&](uint32_t (&v)[32], int c) {
-          mask(v, c);
+        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
+        uint64_t sum0 = 0, sum1 = 0;  // two fp32 sums each
+#pragma unroll 1
+        for (int c = 0; c < kKeys; c += 32) {
+          tmem_ld32(v, ts + c);
+          wait_ld();
+          keep_ld(v);
+          if (!clear) hide(v, seen_bits(c, hi, lo, sk, pages));
           uint32_t p[16];
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
-            const float p0 = exp2_fast(fmaf(__uint_as_float(v[k]), a.scale_log2, -ref));
-            const float p1 = exp2_fast(fmaf(__uint_as_float(v[k + 1]), a.scale_log2, -ref));
-            sum[k & 2] += p0;
-            sum[(k & 2) + 1] += p1;
+            const uint64_t x2 = fma2((uint64_t)v[k + 1] << 32 | v[k], scale2, ref2);
+            const float p0 = exp2_fast(__uint_as_float((uint32_t)x2));
+            const float p1 = exp2_fast(__uint_as_float((uint32_t)(x2 >> 32)));
+            if (k & 2) sum1 = add2(sum1, pack2(p0, p1));
+            else sum0 = add2(sum0, pack2(p0, p1));
             const __half2 h = __floats2half2_rn(p0, p1);
             p[k >> 1] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          tmem_st16(ts + 16 * c, p);
-        };
-        tmem_ld32(v1, ts + 32);
-        wait_ld();
-        keep_ld(v1);
-        weights(v0, 0);
-        tmem_ld32(v0, ts + 64);
-        weights(v1, 1);
-        wait_ld();
-        keep_ld(v0);
-        tmem_ld32(v1, ts + 96);
-        weights(v0, 2);
-        wait_ld();
-        keep_ld(v1);
-        weights(v1, 3);
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          // columns c / 2 .. of P lie over scores that have been read by now
+          tmem_st16(ts + (c >> 1), p);
+        }
+        sum0 = add2(sum0, sum1);
+        l += __uint_as_float((uint32_t)sum0) + __uint_as_float((uint32_t)(sum0 >> 32));
         wait_st();
         fence_before();
         __syncwarp();
