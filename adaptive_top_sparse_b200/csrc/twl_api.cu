@@ -604,7 +604,7 @@ twl_status twl_window_prefill(const void* q, const int32_t* q_start, int32_t tot
   // a row of 128 values of the cache is a coordinate of the copies: 31 bits
   if ((uint64_t)k.num_phys * (uint64_t)k.hkv * kPage > 0x7FFFFFFFull) return TWL_ERR_UNSUPPORTED;
   if (total_q < 0 || !q_start || !aligned(q_start, 4)) return TWL_ERR_INVALID_ARG;
-  if (total_q > 0 && (!q || !o || !lse || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4)))
+  if (total_q > 0 && (!q || !o || !lse || !aligned(q, 16) || !aligned(o, 32) || !aligned(lse, 4)))
     return TWL_ERR_INVALID_ARG;
   if ((long long)k.batch * k.hkv > 4096) return TWL_ERR_UNSUPPORTED;
   Carve c{static_cast<char*>(ws)};

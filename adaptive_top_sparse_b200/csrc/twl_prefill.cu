@@ -50,7 +50,7 @@ struct Smem {
   // barriers
   uint64_t q_full, q_free;
   uint64_t full[kBufs], empty[kBufs];
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
   uint64_t v_ready[kBufs];  // V of the buffer is loaded and its unseen rows are zero
   uint32_t tmem;
   int aborted;
@@ -82,6 +82,14 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
       "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
       " selp.b32 %0, 1, 0, p;\n}\n"
       : "=r"(ok) : "r"(sptr(b)), "r"(parity), "r"(20000u) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool bar_try_now(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.b32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(sptr(b)), "r"(parity) : "memory");
   return ok != 0;
 }
 constexpr uint32_t kWaitLimit = 1u << 16;  // polls of up to 20 us each
@@ -177,6 +185,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
 __device__ __forceinline__ void keep_ld(uint32_t (&r)[32]) {
   asm volatile("" : TWL_R8(r, 0), TWL_R8(r, 8), TWL_R8(r, 16), TWL_R8(r, 24));
 }
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31, %32};" ::"r"(addr),
+      TWL_I8(r, 0), TWL_I8(r, 8), TWL_I8(r, 16), TWL_I8(r, 24) : "memory");
+}
 __device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -189,6 +204,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
       "%11, %12, %13, %14, %15, %16};" ::"r"(addr), TWL_I8(r, 0), TWL_I8(r, 8) : "memory");
+}
+
+// 32 bytes, a whole sector (the rows of a warp's lanes are far apart).
+__device__ __forceinline__ void st_global32(void* dst, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), TWL_I8(r, 0)
+               : "memory");
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -214,6 +235,25 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t y;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
   return y;
+}
+// 2^x of a pair without the special function unit, whose 16 results a cycle are as much of a bound
+// as the tensor core (1100 against 1072 cycles a tile): x = i + f with f in [-0.5, 0.5] by rounding
+// through 1.5 2^23, 2^f by a polynomial (degree 4, fitted for the least relative error, 2.7e-6), i
+// added to the exponent.  Below 2^-125 the result stays there: 0 as fp16.
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
+  const uint64_t magic = pack2(0x1.8p23f, 0x1.8p23f), unmagic = pack2(-0x1.8p23f, -0x1.8p23f);
+  x = pack2(fmaxf(__uint_as_float((uint32_t)x), -125.f),
+            fmaxf(__uint_as_float((uint32_t)(x >> 32)), -125.f));
+  const uint64_t i = add2(x, magic);
+  const uint64_t f = fma2(add2(i, unmagic), pack2(-1.f, -1.f), x);
+  uint64_t y = fma2(f, pack2(0.009570102207362652f, 0.009570102207362652f),
+                    pack2(0.05591785907745361f, 0.05591785907745361f));
+  y = fma2(y, f, pack2(0.240247443318367f, 0.240247443318367f));
+  y = fma2(y, f, pack2(0.6931217908859253f, 0.6931217908859253f));
+  y = fma2(y, f, pack2(0.9999992847442627f, 0.9999992847442627f));
+  const uint32_t lo = (uint32_t)y + ((uint32_t)i << 23);
+  const uint32_t hi = (uint32_t)(y >> 32) + ((uint32_t)(i >> 32) << 23);
+  return (uint64_t)hi << 32 | lo;
 }
 // The lowest n of 32 bits (none for n <= 0).
 __device__ __forceinline__ uint32_t low_bits(int n) {
@@ -404,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kBufs; ++i) bar_init(&sm.full[i], 1), bar_init(&sm.empty[i], 2);
     for (int x = 0; x < 2; ++x) {
       bar_init(&sm.s_full[x], 1);
+      bar_init(&sm.p_half[x], 4);
       bar_init(&sm.p_full[x], 4);
       bar_init(&sm.o_full[x], 1);
       bar_init(&sm.o_free[x], 4);
@@ -481,63 +522,94 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ================================================================ tensor core
+    // One thread walks, waits and issues.  What it does between two products is time the tensor core
+    // may idle, so ring places and phases are kept as running values (no division), and everything
+    // a product needs but its weights has been waited for while the product before it ran.
     if (lane == 0) {
-      int kfill = 0, nseg = 0;
-      uint32_t pph[2] = {0, 0};
-      int units[2] = {0, 0};
       bool ok = true;
-      auto scores = [&](int x, uint32_t kaddr) {
+      uint32_t full_ph = 0, ready_ph = 0, p_ph = 0, free_ph = 0, q_ph = 0;
+      int kb = 0, units[2] = {0, 0};  // buffer of the next K
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!bar_try_now(bar, parity)) ok = ok && bar_wait(sm, bar, parity, a.flags);
+      };
+      auto next_buf = [](int b) { return b + 1 == kBufs ? 0 : b + 1; };
+      auto wait_k = [&](int b) {
+        wait(&sm.full[b], full_ph >> b & 1);
+        full_ph ^= 1u << b;
+      };
+      auto wait_v = [&](int b) {  // a buffer takes K and V in turn
+        wait(&sm.v_ready[b], ready_ph >> b & 1);
+        ready_ph ^= 1u << b;
+        full_ph ^= 1u << b;
+      };
+      const uint64_t dq = smem_desc(sptr(qbuf), 16, 1024), dk = smem_desc(sptr(ring), 16, 1024),
+                     dv = smem_desc(sptr(ring), 16384, 1024);
+      auto scores = [&](int x, int b) {
+        const uint64_t a0 = dq + (uint64_t)(x * (32768 >> 4)),
+                       b0 = dk + (uint64_t)(b * (kBufBytes >> 4));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-          mma_ss(tmem + x * 128, smem_desc(sptr(qbuf) + x * 32768 + off, 16, 1024),
-                 smem_desc(kaddr + off, 16, 1024), k > 0);
+          const uint64_t off = (k >> 2) * (16384 >> 4) + (k & 3) * (32 >> 4);
+          mma_ss(tmem + x * 128, a0 + off, b0 + off, k > 0);
         }
         mma_commit(&sm.s_full[x]);
       };
-      auto wait_fill = [&](int f) {
-        return bar_wait(sm, &sm.full[f % kBufs], (f / kBufs) & 1, a.flags);
-      };
-      auto addr_of = [&](int f) { return sptr(ring) + (f % kBufs) * kBufBytes; };
       while (ok && w.next()) {
-        const int xs = w.two ? 2 : 1;
-        ok = bar_wait(sm, &sm.q_full, nseg & 1, a.flags) && wait_fill(kfill);
-        ++nseg;
+        const bool two = w.two;
+        wait(&sm.q_full, q_ph);
+        q_ph ^= 1;
+        wait_k(kb);
         if (!ok) break;
         fence_after();
-        for (int x = 0; x < xs; ++x) scores(x, addr_of(kfill));
-        mma_commit(&sm.empty[kfill % kBufs]);
+        scores(0, kb);
+        if (two) scores(1, kb);
+        mma_commit(&sm.empty[kb]);
         if (w.tiles == 1) mma_commit(&sm.q_free);
-        for (int i = 0; i < w.tiles && ok; ++i, kfill += 2) {
-          const int vf = kfill + 1;
-          for (int x = 0; x < xs; ++x) {
-            ok = bar_wait(sm, &sm.p_full[x], pph[x], a.flags);
-            pph[x] ^= 1;
-            if (ok && i == 0 && units[x] > 0)
-              ok = bar_wait(sm, &sm.o_free[x], (units[x] - 1) & 1, a.flags);
-            if (ok && x == 0) {
-              // a buffer takes K and V in turn: its n-th V is fill (2 n + const) kBufs + buffer
-              ok = bar_wait(sm, &sm.v_ready[vf % kBufs], (vf / (2 * kBufs)) & 1, a.flags);
+        wait_v(next_buf(kb));
+        for (int i = w.tiles; i > 0 && ok; --i) {
+          const int vb = next_buf(kb), kn = next_buf(vb);
+          const uint64_t v0 = dv + (uint64_t)(vb * (kBufBytes >> 4));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (x == 1 && !two) break;
+            if (i == w.tiles && units[x] > 0) {
+              wait(&sm.o_free[x], free_ph >> x & 1);
+              free_ph ^= 1u << x;
             }
+            const uint32_t ph = p_ph >> x & 1;
+            p_ph ^= 1u << x;
+            const bool all = bar_try_now(&sm.p_full[x], ph);
+            if (!all) wait(&sm.p_half[x], ph);
             if (!ok) break;
             fence_after();
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8,
-                     smem_desc(addr_of(vf) + k * 2048, 16384, 1024), i > 0 || k > 0);
-            if (i + 1 == w.tiles) {
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + 8 * k, v0 + k * (2048 >> 4),
+                     i < w.tiles || k > 0);
+            if (!all) {
+              wait(&sm.p_full[x], ph);
+              if (!ok) break;
+              fence_after();
+            }
+#pragma unroll
+            for (int k = 4; k < 8; ++k)
+              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + 8 * k, v0 + k * (2048 >> 4), true);
+            const bool last = x == 1 || !two;  // query tile
+            if (last) mma_commit(&sm.empty[vb]);
+            if (i == 1) {
               mma_commit(&sm.o_full[x]);
               ++units[x];
             } else {
-              if (x == 0) ok = wait_fill(kfill + 2);
+              if (x == 0) wait_k(kn);
+              if (last) wait_v(next_buf(kn));
               if (!ok) break;
-              scores(x, addr_of(kfill + 2));
+              scores(x, kn);
             }
           }
           if (!ok) break;
-          mma_commit(&sm.empty[vf % kBufs]);
-          if (i + 1 < w.tiles) mma_commit(&sm.empty[(kfill + 2) % kBufs]);
-          if (i + 2 == w.tiles) mma_commit(&sm.q_free);
+          if (i > 1) mma_commit(&sm.empty[kn]);
+          if (i == 2) mma_commit(&sm.q_free);
+          kb = kn;
         }
       }
     }
@@ -606,18 +678,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         // cache (unrolled over the row, half of the softmax warps' time went to fetching them).
         uint32_t v[32];
         float m0 = -INFINITY, m1 = -INFINITY;
+        int dark = 0;
 #pragma unroll 1
         for (int c = 0; c < kKeys; c += 32) {
           tmem_ld32(v, ts + c);
           wait_ld();
           keep_ld(v);
-          if (!clear) hide(v, seen_bits(c, hi, lo, sk, pages));
+          if (!clear) {
+            // hidden scores become -inf here, in TMEM too; columns no row of the warp sees are
+            // skipped from here on
+            const uint32_t seen = seen_bits(c, hi, lo, sk, pages);
+            if (!__any_sync(0xffffffffu, seen != 0)) {
+              dark |= 1 << (c / 32);
+              continue;
+            }
+            hide(v, seen);
+            tmem_st32(ts + c, v);
+          }
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
             m0 = max3(m0, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
             m1 = max3(m1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
           }
         }
+        if (!clear) wait_st();
         const float top = fmaxf(m0, m1) * a.scale_log2;
         if (__any_sync(0xffffffffu, top > m + kSlack)) {
           const float mn = fmaxf(m, top);
@@ -642,23 +726,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t sum0 = 0, sum1 = 0;  // two fp32 sums each
 #pragma unroll 1
         for (int c = 0; c < kKeys; c += 32) {
-          tmem_ld32(v, ts + c);
-          wait_ld();
-          keep_ld(v);
-          if (!clear) hide(v, seen_bits(c, hi, lo, sk, pages));
           uint32_t p[16];
+          if (dark >> (c / 32) & 1) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const uint64_t x2 = fma2((uint64_t)v[k + 1] << 32 | v[k], scale2, ref2);
-            const float p0 = exp2_fast(__uint_as_float((uint32_t)x2));
-            const float p1 = exp2_fast(__uint_as_float((uint32_t)(x2 >> 32)));
-            if (k & 2) sum1 = add2(sum1, pack2(p0, p1));
-            else sum0 = add2(sum0, pack2(p0, p1));
-            const __half2 h = __floats2half2_rn(p0, p1);
-            p[k >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int k = 0; k < 16; ++k) p[k] = 0u;
+          } else {
+            tmem_ld32(v, ts + c);
+            wait_ld();
+            keep_ld(v);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const uint64_t x2 = fma2((uint64_t)v[k + 1] << 32 | v[k], scale2, ref2);
+              // one pair in four by polynomial
+              const uint64_t p2 = (k & 6) == 6
+                                      ? exp2_pair(x2)
+                                      : pack2(exp2_fast(__uint_as_float((uint32_t)x2)),
+                                              exp2_fast(__uint_as_float((uint32_t)(x2 >> 32))));
+              if (k & 2) sum1 = add2(sum1, p2);
+              else sum0 = add2(sum0, p2);
+              const __half2 h = __floats2half2_rn(__uint_as_float((uint32_t)p2),
+                                                  __uint_as_float((uint32_t)(p2 >> 32)));
+              p[k >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+            }
           }
           // columns c / 2 .. of P lie over scores that have been read by now
           tmem_st16(ts + (c >> 1), p);
+          if (c == kKeys / 2 - 32) {  // the product can start on the first half
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm.p_half[x]);
+          }
         }
         sum0 = add2(sum0, sum1);
         l += __uint_as_float((uint32_t)sum0) + __uint_as_float((uint32_t)(sum0 >> 32));
@@ -691,10 +789,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                   __uint_as_float(o[k + 1]) * inv);
               h[k >> 1] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            uint4* dst = reinterpret_cast<uint4*>(a.o + out * kHeadDim + 32 * c);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              dst[k] = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+            uint16_t* dst = a.o + out * kHeadDim + 32 * c;
+            st_global32(dst, h);
+            st_global32(dst + 16, h + 8);
           } else if (valid) {
             uint4* dst = reinterpret_cast<uint4*>(part);
 #pragma unroll

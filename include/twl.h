@@ -350,7 +350,7 @@ twl_status twl_sparse_decode_noalloc(const void* q, int32_t num_q_heads, const t
  *   q_start[b] (a prompt, a chunk of one, or drafted tokens to verify).  Row q_start[b] + i of q
  *   sits at position seq_lens[b] - q_len_b + i; its K and V are in the cache already.
  *   q float16 [total_q][Hq][128]; q_start int32 [B + 1], ascending from >= 0 to <= total_q
- *   o float16 [total_q][Hq][128] out; lse float [total_q][Hq] out
+ *   o float16 [total_q][Hq][128] out, 32-byte aligned; lse float [total_q][Hq] out
  *   Rows of q outside every chunk are not read and their outputs not written.  q_len_b = 0 is
  *   fine.  A sequence whose chunk is not inside [0, total_q] or longer than its length, or whose
  *   length is > 16 * max_pages, is skipped (its outputs are not written), and a page that is out
