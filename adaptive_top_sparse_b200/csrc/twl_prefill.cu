@@ -12,14 +12,14 @@
 // the CTA arriving last merges in run order.  So a few long sequences with a handful of queries
 // use the card as well as one long prompt, and lengths stay on the device.
 //
-// One CTA: eleven warps.
+// One CTA: nineteen warps.
 //   loader     TMA of the queries and of K and V pages (16 rows of 128 bytes a copy, 128-byte
 //              swizzle) into a ring of five 32 KB buffers
 //   fixer      zeroes the V rows nobody in the unit sees (a weight of 0 times a stale infinity
 //              would be NaN); only tiles at the edge of what is seen need it
 //   mma        one thread: S_x = Q_x K^T (tcgen05, fp16 in, fp32 in TMEM) and O_x += P_x V with P
 //              in TMEM over S and V taken as it lies in the page (MN-major)
-//   softmax x  four warps per query tile, a thread per row: scores from TMEM, maximum, weights
+//   softmax x  eight warps per query tile, two threads per row: scores from TMEM, maximum, weights
 //              back to TMEM as fp16, sums in fp32.  While one tile's softmax runs, the tensor core
 //              works for the other.
 // The weights enter the product as fp16 (2^-11 of each, as the fp16 result itself); maxima, sums
@@ -38,11 +38,11 @@ namespace {
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kSlack = 8.f;  // log2: a row's maximum is raised only when exceeded by more
 constexpr int kRows = 256, kTileRows = 128, kKeys = 128;
-constexpr int kThreads = 352;
+constexpr int kThreads = 608;
 constexpr int kBufBytes = 32768, kBufs = 5;
 constexpr int kQBytes = 65536;
 constexpr int kRecs = 8;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kFixWarp = 18;
 // partial of a cut unit: o as [32][256] float4 (column group, row), then max[256], sum[256]
 constexpr int kPartFloats = kRows * 130;
 
@@ -50,7 +50,7 @@ struct Smem {
   // barriers
   uint64_t q_full, q_free;
   uint64_t full[kBufs], empty[kBufs];
-  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t v_ready[kBufs];  // V of the buffer is loaded and its unseen rows are zero
   uint32_t tmem;
   int aborted;
@@ -58,9 +58,9 @@ struct Smem {
   int is_last;
   // where the run starts
   int b, kvh, qt, tile;
-  int red[32];
+  float swap[2][2][kTileRows];  // maxima and sums of the halves of the rows
 };
-constexpr size_t kSmemBytes = 1024 + kQBytes + (size_t)kBufs * kBufBytes + sizeof(Smem);
+constexpr size_t kSmemBytes = kQBytes + (size_t)kBufs * kBufBytes + sizeof(Smem);
 
 // ------------------------------------------------------------------ PTX
 __device__ __forceinline__ uint32_t sptr(const void* p) {
@@ -362,9 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_window_prefill(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap qmap,
                      const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* base_ptr = reinterpret_cast<unsigned char*>(
-      ((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) unsigned char base_ptr[];
   unsigned char* qbuf = base_ptr;
   unsigned char* ring = base_ptr + kQBytes;
   Smem& sm = *reinterpret_cast<Smem*>(ring + (size_t)kBufs * kBufBytes);
@@ -444,10 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kBufs; ++i) bar_init(&sm.full[i], 1), bar_init(&sm.empty[i], 2);
     for (int x = 0; x < 2; ++x) {
       bar_init(&sm.s_full[x], 1);
-      bar_init(&sm.p_half[x], 4);
-      bar_init(&sm.p_full[x], 4);
+      bar_init(&sm.p_full[x], 8);
       bar_init(&sm.o_full[x], 1);
-      bar_init(&sm.o_free[x], 4);
+      bar_init(&sm.o_free[x], 8);
     }
     for (int i = 0; i < kBufs; ++i) bar_init(&sm.v_ready[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -576,24 +573,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               wait(&sm.o_free[x], free_ph >> x & 1);
               free_ph ^= 1u << x;
             }
-            const uint32_t ph = p_ph >> x & 1;
+            wait(&sm.p_full[x], p_ph >> x & 1);
             p_ph ^= 1u << x;
-            const bool all = bar_try_now(&sm.p_full[x], ph);
-            if (!all) wait(&sm.p_half[x], ph);
             if (!ok) break;
             fence_after();
+            // the weights of columns 64 .. lie over those columns' scores
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + 8 * k, v0 + k * (2048 >> 4),
-                     i < w.tiles || k > 0);
-            if (!all) {
-              wait(&sm.p_full[x], ph);
-              if (!ok) break;
-              fence_after();
-            }
-#pragma unroll
-            for (int k = 4; k < 8; ++k)
-              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + 8 * k, v0 + k * (2048 >> 4), true);
+            for (int k = 0; k < 8; ++k)
+              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + (k >> 2) * 64 + (k & 3) * 8,
+                     v0 + k * (2048 >> 4), i < w.tiles || k > 0);
             const bool last = x == 1 || !two;  // query tile
             if (last) mma_commit(&sm.empty[vb]);
             if (i == 1) {
@@ -652,9 +640,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kMmaWarp) {
     // ================================================================ softmax of query tile x
-    const int x = warp >> 2, row = tid & 127;
+    // Two threads per row: columns 64 half .. of the scores, dims 64 half .. of the output.
+    const int x = warp >> 3, half = warp >> 2 & 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * 128;
+    const uint32_t ts = tmem + lanes + x * 128 + half * 64;
+    const uint32_t to = tmem + lanes + 256 + x * 128 + half * 64;
+    const int pair_bar = 2 + x * 4 + (warp & 3);
+    float* mine = &sm.swap[x][half][row];
+    const float* other = &sm.swap[x][half ^ 1][row];
     uint32_t sph = 0, oph = 0;
     int ntile = 0;
     while (w.next()) {
@@ -666,13 +659,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // first and last query of this tile of rows: tiles of keys that all of them see need no mask
       const int ta = w.s.t0 + x * (kTileRows / G), tb = min(ta + kTileRows / G, w.c.n) - 1;
       for (int j = 0; active && j < w.tiles; ++j) {
-        if (!warp_wait(sm, &sm.s_full[x], sph, a.flags)) break;
+        const bool live = warp_wait(sm, &sm.s_full[x], sph, a.flags);
         sph ^= 1;
         fence_after();
         const int base = w.base_of(j), pages = sm.rec[(ntile + j) % kRecs];
         const bool clear = pages == 0xFF && base + kKeys - 1 <= ta &&
                            (base > tb - a.window || base + kKeys <= a.sinks);
-        const int hi = t - base, lo = max(t - a.window, -1) - base, sk = a.sinks - base;
         // A row goes through the loops 32 columns at a time, twice (for its maximum, then for its
         // weights): TMEM answers in some 20 cycles, and loops this short stay in the instruction
         // cache (unrolled over the row, half of the softmax warps' time went to fetching them).
@@ -680,14 +672,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m0 = -INFINITY, m1 = -INFINITY;
         int dark = 0;
 #pragma unroll 1
-        for (int c = 0; c < kKeys; c += 32) {
+        for (int c = 0; live && c < 64; c += 32) {
           tmem_ld32(v, ts + c);
           wait_ld();
           keep_ld(v);
           if (!clear) {
             // hidden scores become -inf here, in TMEM too; columns no row of the warp sees are
             // skipped from here on
-            const uint32_t seen = seen_bits(c, hi, lo, sk, pages);
+            const int first = half * 64 + c;
+            const uint32_t seen = seen_bits(first, t - base, max(t - a.window, -1) - base,
+                                            a.sinks - base, pages);
             if (!__any_sync(0xffffffffu, seen != 0)) {
               dark |= 1 << (c / 32);
               continue;
@@ -701,23 +695,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             m1 = max3(m1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
           }
         }
+        m0 = fmaxf(m0, m1);
+        // the halves agree on the row's maximum (they write again only behind the next scores,
+        // which need both of them)
+        *mine = m0;
         if (!clear) wait_st();
-        const float top = fmaxf(m0, m1) * a.scale_log2;
+        named_sync(pair_bar, 64);
+        if (!live) continue;
+        const float top = fmaxf(m0, *other) * a.scale_log2;
         if (__any_sync(0xffffffffu, top > m + kSlack)) {
           const float mn = fmaxf(m, top);
           const float f = exp2_fast(m - ref_of(mn));
           m = mn;
           l *= f;
           if (j > 0) {  // this tile's scores were issued behind the last product into O
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 16) {
               uint32_t o[16];
-              tmem_ld16(o, to + 16 * c);
+              tmem_ld16(o, to + c);
               wait_ld();
               keep_ld16(o);
 #pragma unroll
               for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st16(to + 16 * c, o);
+              tmem_st16(to + c, o);
             }
           }
         }
@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
         uint64_t sum0 = 0, sum1 = 0;  // two fp32 sums each
 #pragma unroll 1
-        for (int c = 0; c < kKeys; c += 32) {
+        for (int c = 0; c < 64; c += 32) {
           uint32_t p[16];
           if (dark >> (c / 32) & 1) {
 #pragma unroll
@@ -749,14 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               p[k >> 1] = *reinterpret_cast<const uint32_t*>(&h);
             }
           }
-          // columns c / 2 .. of P lie over scores that have been read by now
+          // the weights' columns lie over scores of this thread that have been read by now
           tmem_st16(ts + (c >> 1), p);
-          if (c == kKeys / 2 - 32) {  // the product can start on the first half
-            wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(&sm.p_half[x]);
-          }
         }
         sum0 = add2(sum0, sum1);
         l += __uint_as_float((uint32_t)sum0) + __uint_as_float((uint32_t)(sum0 >> 32));
@@ -767,6 +761,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ntile += w.tiles;
       // ---- the unit's rows
+      *mine = l;
+      named_sync(pair_bar, 64);
+      l += *other;
+      named_sync(pair_bar, 64);
       if (active && warp_wait(sm, &sm.o_full[x], oph, a.flags)) fence_after();
       if (active) oph ^= 1;
       const bool fine = !__any_sync(0xffffffffu, dead());
@@ -776,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (active && fine) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t o[32];
           tmem_ld32(o, to + 32 * c);
           wait_ld();
@@ -789,14 +787,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                   __uint_as_float(o[k + 1]) * inv);
               h[k >> 1] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            uint16_t* dst = a.o + out * kHeadDim + 32 * c;
+            uint16_t* dst = a.o + out * kHeadDim + 64 * half + 32 * c;
             st_global32(dst, h);
             st_global32(dst + 16, h + 8);
           } else if (valid) {
             uint4* dst = reinterpret_cast<uint4*>(part);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              dst[(8 * c + k) * kRows + prow] =
+              dst[(16 * half + 8 * c + k) * kRows + prow] =
                   make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
           __syncwarp();
@@ -804,9 +802,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(&sm.o_free[x]);
-        if (valid && w.whole)
+        if (valid && w.whole && half == 0)
           a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        if (valid && !w.whole) {
+        if (valid && !w.whole && half == 0) {
           part[kRows * kHeadDim + prow] = m;
           part[kRows * (kHeadDim + 1) + prow] = l;
         }
@@ -817,17 +815,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = (int)(((fs + 1) * runs - 1) / total);
       const int last = (int)(((fs + w.s.tiles) * runs - 1) / total);
       __threadfence();
-      named_sync(1, 256);
+      named_sync(1, 512);
       if (tid == 0)
         sm.is_last = !dead() && atomicAdd(a.done + first, 1u) == (unsigned)(last - first);
-      named_sync(1, 256);
+      named_sync(1, 512);
       if (sm.is_last) {
         __threadfence();
         const int rows = min(kRows, (w.c.qn - w.i0) * G);
         auto at = [&](int r) {  // the unit starts in run `first`: its second slot
           return a.part + ((size_t)r * 2 + (r == first ? 1 : 0)) * kPartFloats;
         };
-        for (int e = tid; e < rows * 32; e += 256) {
+        for (int e = tid; e < rows * 32; e += 512) {
           const int r = e % rows, c = e / rows;
           float mm = -INFINITY;
           for (int k = first; k <= last; ++k) mm = fmaxf(mm, __ldcg(at(k) + kRows * kHeadDim + r));
@@ -852,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (tid == 0) a.done[first] = 0u;
       }
-      named_sync(1, 256);
+      named_sync(1, 512);
     }
   }
   fence_before();
