@@ -54,7 +54,7 @@ struct Smem {
   uint64_t v_ready[kBufs];  // V of the buffer is loaded and its unseen rows are zero
   uint32_t tmem;
   int aborted;
-  int rec[kRecs];  // pages of a key tile that were loaded (bit per page)
+  int rec[kRecs];  // of a key tile: pages that were loaded (bit per page), its number << 8
   int is_last;
   // where the run starts
   int b, kvh, qt, tile;
@@ -106,6 +106,7 @@ __device__ __forceinline__ bool bar_wait(Smem& s, uint64_t* b, uint32_t parity, 
 }
 // The same for a converged warp, with one answer for all of its lanes.
 __device__ __forceinline__ bool warp_wait(Smem& s, uint64_t* b, uint32_t parity, uint32_t* flags) {
+  if (__all_sync(0xffffffffu, bar_try_now(b, parity))) return true;
   return __all_sync(0xffffffffu, bar_wait(s, b, parity, flags));
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -217,6 +218,20 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 2^x without the special function unit, whose one result in 8 cycles a warp is as much of a bound
+// as the tensor core: x = i + f with f in [-0.5, 0.5] by rounding through 1.5 2^23, 2^f by a
+// polynomial (degree 4, fitted for the least relative error, 2.7e-6), i added to the exponent.
+// Below 2^-125 the result stays there: 0 as fp16.
+__device__ __forceinline__ float exp2_poly(float x) {
+  x = fmaxf(x, -125.f);
+  const float i = __fadd_rn(x, 0x1.8p23f);
+  const float f = x - __fsub_rn(i, 0x1.8p23f);
+  float y = fmaf(f, 0.009570102207362652f, 0.05591785907745361f);
+  y = fmaf(y, f, 0.240247443318367f);
+  y = fmaf(y, f, 0.6931217908859253f);
+  y = fmaf(y, f, 0.9999992847442627f);
+  return __uint_as_float(__float_as_uint(y) + (__float_as_uint(i) << 23));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
@@ -236,24 +251,20 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
   return y;
 }
-// 2^x of a pair without the special function unit, whose 16 results a cycle are as much of a bound
-// as the tensor core (1100 against 1072 cycles a tile): x = i + f with f in [-0.5, 0.5] by rounding
-// through 1.5 2^23, 2^f by a polynomial (degree 4, fitted for the least relative error, 2.7e-6), i
-// added to the exponent.  Below 2^-125 the result stays there: 0 as fp16.
-__device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
-  const uint64_t magic = pack2(0x1.8p23f, 0x1.8p23f), unmagic = pack2(-0x1.8p23f, -0x1.8p23f);
-  x = pack2(fmaxf(__uint_as_float((uint32_t)x), -125.f),
-            fmaxf(__uint_as_float((uint32_t)(x >> 32)), -125.f));
-  const uint64_t i = add2(x, magic);
-  const uint64_t f = fma2(add2(i, unmagic), pack2(-1.f, -1.f), x);
-  uint64_t y = fma2(f, pack2(0.009570102207362652f, 0.009570102207362652f),
-                    pack2(0.05591785907745361f, 0.05591785907745361f));
-  y = fma2(y, f, pack2(0.240247443318367f, 0.240247443318367f));
-  y = fma2(y, f, pack2(0.6931217908859253f, 0.6931217908859253f));
-  y = fma2(y, f, pack2(0.9999992847442627f, 0.9999992847442627f));
-  const uint32_t lo = (uint32_t)y + ((uint32_t)i << 23);
-  const uint32_t hi = (uint32_t)(y >> 32) + ((uint32_t)(i >> 32) << 23);
-  return (uint64_t)hi << 32 | lo;
+// Weights of 32 scores, as fp16 pairs, and their sums (two in a pair).  One in eight by polynomial:
+// then the special function unit and the instruction issue are about even.
+__device__ __forceinline__ void weights(const uint32_t (&v)[32], uint64_t scale, uint64_t shift,
+                                        uint64_t& sum, uint32_t (&p)[16]) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    const uint64_t x = fma2((uint64_t)v[k + 1] << 32 | v[k], scale, shift);
+    const float x0 = __uint_as_float((uint32_t)x), x1 = __uint_as_float((uint32_t)(x >> 32));
+    const float p0 = exp2_fast(x0);
+    const float p1 = (k & 6) == 6 ? exp2_poly(x1) : exp2_fast(x1);
+    sum = add2(sum, pack2(p0, p1));
+    const __half2 h = __floats2half2_rn(p0, p1);
+    p[k >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+  }
 }
 // The lowest n of 32 bits (none for n <= 0).
 __device__ __forceinline__ uint32_t low_bits(int n) {
@@ -496,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           if (lane == 0) {
-            if (kv == 0) sm.rec[ntile % kRecs] = (int)pages;
+            if (kv == 0) sm.rec[ntile % kRecs] = (int)pages | (base / kKeys) << 8;
             bar_expect(&sm.full[buf], __popc(pages) * 4096);
           }
           __syncwarp();
@@ -612,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int buf = fill % kBufs;
           ok = warp_wait(sm, &sm.full[buf], (fill / kBufs) & 1, a.flags);
           if (!ok) break;
-          const int base = w.base_of(i), pages = sm.rec[ntile % kRecs];
+          const int rec = sm.rec[ntile % kRecs], base = (rec >> 8) * kKeys, pages = rec & 0xFF;
           if (kv == 1 && w.ragged(base, pages)) {
             for (int r = lane; r < kKeys; r += 32) {
               const int key = base + r;
@@ -649,12 +660,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* mine = &sm.swap[x][half][row];
     const float* other = &sm.swap[x][half ^ 1][row];
     uint32_t sph = 0, oph = 0;
-    int ntile = 0;
+    uint32_t ntile = 0;  // key tiles so far, of the CTA
     while (w.next()) {
       const int i = w.i0 + (x * kTileRows + row) / G;  // the row's query
       const int t = w.c.n - w.c.qn + i;
       const bool active = x == 0 || w.two;
       const bool valid = i < w.c.qn;
+      if (!active) ntile += w.tiles;
       float m = -INFINITY, l = 0.f;
       // first and last query of this tile of rows: tiles of keys that all of them see need no mask
       const int ta = w.s.t0 + x * (kTileRows / G), tb = min(ta + kTileRows / G, w.c.n) - 1;
@@ -662,25 +674,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool live = warp_wait(sm, &sm.s_full[x], sph, a.flags);
         sph ^= 1;
         fence_after();
-        const int base = w.base_of(j), pages = sm.rec[(ntile + j) % kRecs];
+        const int rec = sm.rec[ntile++ % kRecs], base = (rec >> 8) * kKeys, pages = rec & 0xFF;
         const bool clear = pages == 0xFF && base + kKeys - 1 <= ta &&
                            (base > tb - a.window || base + kKeys <= a.sinks);
-        // A row goes through the loops 32 columns at a time, twice (for its maximum, then for its
-        // weights): TMEM answers in some 20 cycles, and loops this short stay in the instruction
-        // cache (unrolled over the row, half of the softmax warps' time went to fetching them).
-        uint32_t v[32];
+        // The columns are read twice, for their maximum and for their weights, and the weights' loop
+        // is kept short: with the row unrolled, half of the softmax warps' time went to fetching
+        // instructions.
         float m0 = -INFINITY, m1 = -INFINITY;
         int dark = 0;
-#pragma unroll 1
-        for (int c = 0; live && c < 64; c += 32) {
-          tmem_ld32(v, ts + c);
+        if (clear) {
+          uint32_t v0[32], v1[32];
+          tmem_ld32(v0, ts);
+          tmem_ld32(v1, ts + 32);
           wait_ld();
-          keep_ld(v);
-          if (!clear) {
+          keep_ld(v0);
+          keep_ld(v1);
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            m0 = max3(m0, __uint_as_float(v0[k]), __uint_as_float(v0[k + 1]));
+            m1 = max3(m1, __uint_as_float(v1[k]), __uint_as_float(v1[k + 1]));
+          }
+        } else if (live) {
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(v, ts + c);
+            wait_ld();
+            keep_ld(v);
             // hidden scores become -inf here, in TMEM too; columns no row of the warp sees are
             // skipped from here on
-            const int first = half * 64 + c;
-            const uint32_t seen = seen_bits(first, t - base, max(t - a.window, -1) - base,
+            const uint32_t seen = seen_bits(half * 64 + c, t - base, max(t - a.window, -1) - base,
                                             a.sinks - base, pages);
             if (!__any_sync(0xffffffffu, seen != 0)) {
               dark |= 1 << (c / 32);
@@ -688,18 +711,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             hide(v, seen);
             tmem_st32(ts + c, v);
-          }
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            m0 = max3(m0, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-            m1 = max3(m1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+            for (int k = 0; k < 32; k += 4) {
+              m0 = max3(m0, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+              m1 = max3(m1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+            }
           }
+          wait_st();
         }
         m0 = fmaxf(m0, m1);
         // the halves agree on the row's maximum (they write again only behind the next scores,
         // which need both of them)
         *mine = m0;
-        if (!clear) wait_st();
         named_sync(pair_bar, 64);
         if (!live) continue;
         const float top = fmaxf(m0, *other) * a.scale_log2;
@@ -722,8 +745,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float ref = ref_of(m);
-        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), ref2 = pack2(-ref, -ref);
-        uint64_t sum0 = 0, sum1 = 0;  // two fp32 sums each
+        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), shift2 = pack2(-ref, -ref);
+        uint64_t sum = 0;
 #pragma unroll 1
         for (int c = 0; c < 64; c += 32) {
           uint32_t p[16];
@@ -731,35 +754,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 16; ++k) p[k] = 0u;
           } else {
+            uint32_t v[32];
             tmem_ld32(v, ts + c);
             wait_ld();
             keep_ld(v);
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const uint64_t x2 = fma2((uint64_t)v[k + 1] << 32 | v[k], scale2, ref2);
-              // one pair in four by polynomial
-              const uint64_t p2 = (k & 6) == 6
-                                      ? exp2_pair(x2)
-                                      : pack2(exp2_fast(__uint_as_float((uint32_t)x2)),
-                                              exp2_fast(__uint_as_float((uint32_t)(x2 >> 32))));
-              if (k & 2) sum1 = add2(sum1, p2);
-              else sum0 = add2(sum0, p2);
-              const __half2 h = __floats2half2_rn(__uint_as_float((uint32_t)p2),
-                                                  __uint_as_float((uint32_t)(p2 >> 32)));
-              p[k >> 1] = *reinterpret_cast<const uint32_t*>(&h);
-            }
+            weights(v, scale2, shift2, sum, p);
           }
           // the weights' columns lie over scores of this thread that have been read by now
           tmem_st16(ts + (c >> 1), p);
         }
-        sum0 = add2(sum0, sum1);
-        l += __uint_as_float((uint32_t)sum0) + __uint_as_float((uint32_t)(sum0 >> 32));
+        l += __uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32));
         wait_st();
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(&sm.p_full[x]);
       }
-      ntile += w.tiles;
       // ---- the unit's rows
       *mine = l;
       named_sync(pair_bar, 64);
