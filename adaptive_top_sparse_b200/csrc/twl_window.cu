@@ -36,7 +36,10 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // units): weights stay below 2^8, far from fp16's largest value, and most tiles skip the rescale.
 constexpr float kSlack = 8.f;
 // Where a 4-bit code meets the tensor core as fp16 (see k_window_decode): two per word.
-constexpr uint32_t kHigh = 0x07800780u, kLow = 0x00F000F0u;
+constexpr uint32_t kNibble = 0x00F000F0u;
+// The maximum of a head that has seen nothing: finite, so that no difference with it is NaN, and
+// below every score of fp16 rows.
+constexpr float kNone = -1e30f;
 constexpr int kPartStride = 132;  // floats of one head's partial: o[128], max, sum, pad
 
 template <bool INT4>
@@ -153,7 +156,7 @@ struct State {
 
 __device__ __forceinline__ void reset(State& st) {
 #pragma unroll
-  for (int c = 0; c < 2; ++c) st.m[c] = -INFINITY, st.l[c] = 0.f, st.z[c] = 0.f;
+  for (int c = 0; c < 2; ++c) st.m[c] = kNone, st.l[c] = 0.f, st.z[c] = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -168,14 +171,9 @@ __device__ __forceinline__ void scale_state(State& st, float f0, float f1) {
   }
 }
 
-// 0 in place of -inf: the reference of a head that has seen nothing (every weight 2^(-inf) = 0).
-__device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f : m; }
-
-// Raises the maxima to cover the tile's t values (t[0], t[1]: token g, heads 2t, 2t + 1; t[2],
-// t[3]: token g + 8) when one exceeds them by more than the slack.
-__device__ __forceinline__ void update_max(State& st, const float (&t)[4]) {
-  const bool need = fmaxf(t[0], t[2]) > st.m[0] + kSlack || fmaxf(t[1], t[3]) > st.m[1] + kSlack;
-  if (!__any_sync(0xffffffffu, need)) return;
+// Raises the maxima to cover the tile's values t (t[0], t[1]: token g, heads 2t, 2t + 1; t[2],
+// t[3]: token g + 8).
+__device__ __forceinline__ void raise_max(State& st, const float (&t)[4]) {
   float f[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
@@ -184,10 +182,14 @@ __device__ __forceinline__ void update_max(State& st, const float (&t)[4]) {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
     const float m = fmaxf(st.m[c], x);
-    f[c] = exp2_fast(st.m[c] - ref_of(m));
+    f[c] = exp2_fast(st.m[c] - m);
     st.m[c] = m;
   }
   scale_state(st, f[0], f[1]);
+}
+
+__device__ __forceinline__ float max4(const float (&v)[4]) {
+  return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
 }
 
 // P^T fragments (hi and lo parts) of the weights w (same order as t in update_max).
@@ -248,7 +250,10 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
     for (int i = tid; i < a.hq; i += blockDim.x) a.lse[(size_t)b * a.hq + i] = -INFINITY;
   }
 
-  const int runs = min((int)gridDim.x, total);
+  // A run has at least a tile for every warp (fewer partials to merge), unless the groups are
+  // smaller than that.
+  const int runs = min(min((int)gridDim.x, total),
+                       max((total + kWarps - 1) / kWarps, a.batch * a.hkv));
   const int run = blockIdx.x;
   if (run < runs) {
     const int f0 = (int)((long long)total * run / runs);
@@ -267,6 +272,8 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
       if (lf >= lgp.ge) lgp = group_of(a, prefix, lf);
       return a.page_table[(size_t)lgp.b * a.max_pages + page_of(lgp, lf)];
     };
+    const int v_dst = 1024 + v_slot(lane >> 2, lane & 3) * 16;
+    const uint32_t* sz_src = (lane < 4 ? a.ksz : a.vsz) + 4 * (lane & 3);
     int phys = fetch_phys();
     auto issue = [&]() {
       if (lf < f1) {
@@ -279,16 +286,13 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
         unsigned char* st = my_ring + ls * kTile;
         const size_t row0 = ok ? ((size_t)phys * a.hkv + lgp.kvh) * kPage : 0;
         if constexpr (INT4) {
-#pragma unroll
-          for (int it = 0; it < 2; ++it) {
-            const int r = it * 8 + (lane >> 2), c = lane & 3;
-            cp_async16(st + r * 64 + c * 16, a.kc + (row0 + r) * 64 + c * 16, ok);
-            cp_async16(st + 1024 + v_slot(r, c) * 16, a.vc + (row0 + r) * 64 + c * 16, ok);
-          }
-          if (lane < 8) {
-            const uint32_t* src = (lane < 4 ? a.ksz : a.vsz) + row0 + 4 * (lane & 3);
-            cp_async16(st + 2048 + lane * 16, src, ok);
-          }
+          const uint8_t* ks = a.kc + row0 * 64 + lane * 16;
+          const uint8_t* vs = a.vc + row0 * 64 + lane * 16;
+          cp_async16(st + lane * 16, ks, ok);
+          cp_async16(st + lane * 16 + 512, ks + 512, ok);
+          cp_async16(st + v_dst, vs, ok);
+          cp_async16(st + v_dst + 512, vs + 512, ok);  // rows r and r + 8 lie 512 bytes apart
+          if (lane < 8) cp_async16(st + 2048 + lane * 16, sz_src + row0, ok);
         } else {
           const int c = lane & 15;
 #pragma unroll
@@ -319,6 +323,7 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
       // ---- the group's queries as the B operand: column = head (G <= 4: heads 0-3 twice)
       uint32_t qb[16];
       float qsum[2] = {0.f, 0.f};
+      const float scale_k = a.scale_log2 * 0x1p20f;  // codes meet q as c 2^-20
       {
         const int h = G == 8 ? lg : (lg & 3);
         const uint16_t* qr = a.q + ((size_t)g.b * a.hq + g.kvh * G + h) * kHeadDim;
@@ -364,9 +369,7 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
         const int base = tile_base[warp][cs];
         cs = cs + 1 == kStages ? 0 : cs + 1;
         if (base < 0) continue;
-        const int k0 = base + lg, k1 = k0 + 8;
-        const bool see0 = k0 < g.n && (k0 < a.sinks || k0 >= g.lo);
-        const bool see1 = k1 < g.n && (k1 < a.sinks || k1 >= g.lo);
+        const bool clear = base + kPage <= g.n && (base >= g.lo || base + kPage <= a.sinks);
         float x[4], w[4];
         if constexpr (INT4) {
           uint32_t* ksz = reinterpret_cast<uint32_t*>(tile + 2048);
@@ -388,54 +391,68 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
             if (lane == 0) a.vsz[row] = sz, vsz[r] = sz;
             __syncwarp();
           }
-          // A 4-bit code c at bits 7-10 of a half is the fp16 value c 2^-17, at bits 4-7 c 2^-20
-          // (fp16 is linear in its bits up to 2^11: subnormals and the first binade).  Not at bits
-          // 0-3: the tensor core aligns products by exponent, and ten leading zeros of a
-          // subnormal cost the sum ten bits (measured: 6e-5 instead of 1e-6 of max|v|).
+          // A 4-bit code c at bits 4-7 of a half is the fp16 value c 2^-20 (fp16 is linear in its
+          // bits up to 2^11).  Not at bits 0-3, where it is c 2^-24: the tensor core aligns products
+          // by exponent, and ten leading zeros of a subnormal cost the sum ten bits (measured: 6e-5
+          // instead of 1e-6 of max|v|).
           float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
           const uint4 ra = *reinterpret_cast<const uint4*>(tile + lg * 64 + lt * 16);
           const uint4 rb = *reinterpret_cast<const uint4*>(tile + (lg + 8) * 64 + lt * 16);
           const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t a0[4] = {wa[i] << 7 & kHigh, wb[i] << 7 & kHigh, wa[i] >> 1 & kHigh,
-                                    wb[i] >> 1 & kHigh};
-            const uint32_t a1[4] = {wa[i] & kLow, wb[i] & kLow, wa[i] >> 8 & kLow,
-                                    wb[i] >> 8 & kLow};
+            const uint32_t a0[4] = {wa[i] << 4 & kNibble, wb[i] << 4 & kNibble,
+                                    wa[i] >> 4 & kNibble, wb[i] >> 4 & kNibble};
+            const uint32_t a1[4] = {wa[i] & kNibble, wb[i] & kNibble, wa[i] >> 8 & kNibble,
+                                    wb[i] >> 8 & kNibble};
             mma_16816(s0, a0, qb[4 * i], qb[4 * i + 1]);
             mma_16816(s1, a1, qb[4 * i + 2], qb[4 * i + 3]);
           }
-          float sv[2], zv[2], t[4];
+          float sv[2], zv[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const uint32_t kk = ksz[lg + 8 * r], vv = vsz[lg + 8 * r];
-            const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&kk));
-            const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&vv));
-            sv[r] = vf.x, zv[r] = vf.y;
-            const float ks = kf.x * a.scale_log2;
-            // the weight that meets the codes is p s_v: its reference includes s_v's exponent, so
-            // that its fp16 parts keep their 22 bits whatever the scale of V
-            const float e = (float)((int)((vv >> 10) & 31u) - 15);
-            const bool see = r ? see1 : see0;
+            const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(ksz + lg + 8 * r));
+            const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(vsz + lg + 8 * r));
+            sv[r] = vf.x, zv[r] = fmaf(8.f, vf.x, vf.y);  // V's codes enter as c - 8
+            const float ks = kf.x * scale_k;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const float d = fmaf(s1[2 * r + c], 0x1p20f, s0[2 * r + c] * 0x1p17f);
-              x[2 * r + c] = fmaf(ks, d, kf.y * qsum[c]);
-              t[2 * r + c] = see ? x[2 * r + c] + e : -INFINITY;
+            for (int c = 0; c < 2; ++c)
+              x[2 * r + c] = fmaf(ks, s0[2 * r + c] + s1[2 * r + c], kf.y * qsum[c]);
+          }
+          if (!clear) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int key = base + lg + 8 * r;
+              if (!(key < g.n && (key < a.sinks || key >= g.lo))) {
+                x[2 * r] = x[2 * r + 1] = -INFINITY;
+                sv[r] = zv[r] = 0.f;
+              }
             }
           }
-          update_max(st, t);
-          const float m0 = ref_of(st.m[0]), m1 = ref_of(st.m[1]);
+          // The weight that meets V's codes is w = p s_v, so the reference m covers the score and
+          // s_v's exponent: w then stays below 2^9, and its two fp16 parts keep 22 bits whatever
+          // the scale of V.  Checked on the outcome: it is raised for few tiles.
+          float p[4];
+          auto weigh = [&]() {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const bool see = r ? see1 : see0;
-            const float p0 = see ? exp2_fast(x[2 * r] - m0) : 0.f;
-            const float p1 = see ? exp2_fast(x[2 * r + 1] - m1) : 0.f;
-            const float ss = see ? sv[r] : 0.f;
-            const float zz = see ? fmaf(8.f, sv[r], zv[r]) : 0.f;  // codes enter as c - 8
-            st.l[0] += p0, st.l[1] += p1;
-            st.z[0] = fmaf(p0, zz, st.z[0]), st.z[1] = fmaf(p1, zz, st.z[1]);
-            w[2 * r] = p0 * ss, w[2 * r + 1] = p1 * ss;
+            for (int i = 0; i < 4; ++i) {
+              p[i] = exp2_fast(x[i] - st.m[i & 1]);
+              w[i] = p[i] * sv[i >> 1];
+            }
+          };
+          weigh();
+          if (__any_sync(0xffffffffu, max4(w) > 512.f || max4(p) > 0x1p33f)) {
+            float t[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              t[i] = x[i] + (float)max((int)(__float_as_uint(sv[i >> 1]) >> 23) - 127, -24);
+            raise_max(st, t);
+            weigh();
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            st.l[i & 1] += p[i];
+            st.z[i & 1] = fmaf(p[i], zv[i >> 1], st.z[i & 1]);
           }
         } else {
           float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
@@ -450,13 +467,21 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
             mma_16816(s1, fb, qb[2 * kk + 2], qb[2 * kk + 3]);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[i] = (i < 2 ? see0 : see1) ? (s0[i] + s1[i]) * a.scale_log2 : -INFINITY;
-          update_max(st, x);
-          const float m0 = ref_of(st.m[0]), m1 = ref_of(st.m[1]);
+          for (int i = 0; i < 4; ++i) x[i] = (s0[i] + s1[i]) * a.scale_log2;
+          if (!clear) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int key = base + lg + 8 * r;
+              if (!(key < g.n && (key < a.sinks || key >= g.lo)))
+                x[2 * r] = x[2 * r + 1] = -INFINITY;
+            }
+          }
+          if (__any_sync(0xffffffffu, fmaxf(x[0], x[2]) > st.m[0] + kSlack ||
+                                          fmaxf(x[1], x[3]) > st.m[1] + kSlack))
+            raise_max(st, x);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            w[i] = (i < 2 ? see0 : see1) ? exp2_fast(x[i] - (i & 1 ? m1 : m0)) : 0.f;
+            w[i] = exp2_fast(x[i] - st.m[i & 1]);
             st.l[i & 1] += w[i];
           }
         }
@@ -486,8 +511,8 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
           for (int i = 0; i < 8; ++i) {
             const uint32_t xx = i & 1 ? x4[i >> 1] >> 8 : x4[i >> 1];
             const uint32_t yy = i & 1 ? y4[i >> 1] >> 8 : y4[i >> 1];
-            const uint32_t av[4] = {centre(xx & 0x000F000Fu, 0x1p15f), centre(xx & kLow, 0x1p11f),
-                                    centre(yy & 0x000F000Fu, 0x1p15f), centre(yy & kLow, 0x1p11f)};
+            const uint32_t av[4] = {centre(xx & 0x000F000Fu, 0x1p15f), centre(xx & kNibble, 0x1p11f),
+                                    centre(yy & 0x000F000Fu, 0x1p15f), centre(yy & kNibble, 0x1p11f)};
             mma_16816(st.acc[i], av, ph[0], ph[1]);
             if constexpr (G == 8) mma_16816(st.acc[i], av, pl[0], pl[1]);
           }
@@ -530,9 +555,9 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
         float fo[2], fm[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float mo = mine[(32 + c) * 32], m = fmaxf(mo, st.m[c]), r = ref_of(m);
-          fo[c] = exp2_fast(mo - r);
-          fm[c] = exp2_fast(st.m[c] - r);
+          const float mo = mine[(32 + c) * 32], m = fmaxf(mo, st.m[c]);
+          fo[c] = exp2_fast(mo - m);
+          fm[c] = exp2_fast(st.m[c] - m);
           st.m[c] = m;
         }
         scale_state(st, fm[0], fm[1]);
@@ -550,43 +575,63 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
       const bool whole = g.gs >= f0 && g.ge <= f1;
       const int group = g.b * a.hkv + g.kvh;
       float* part = a.part + ((size_t)run * 2 + (g.gs < f0 ? 0 : 1)) * G * kPartStride;
-      for (int e = tid; e < G * kHeadDim; e += kWarps * 32) {
-        const int h = e / kHeadDim, d = e % kHeadDim;
-        int reg, ln;
-        if constexpr (INT4) {  // channel 16 g + 2 i + (row >= 8)
-          reg = ((d & 15) >> 1) * 4 + (d & 1) * 2 + (h & 1);
-          ln = (d >> 4) * 4 + (h >> 1);
-        } else {  // channel 16 i + row
-          reg = (d >> 4) * 4 + ((d >> 3) & 1) * 2 + (h & 1);
-          ln = (d & 7) * 4 + (h >> 1);
-        }
-        const int hl = h >> 1;  // the lane (g = 0) that holds the head's statistics
-        float m = -INFINITY;
+      {
+        // every warp joins 32 / kWarps of the accumulators, each lane its own columns
+        constexpr int kMine = 32 / kWarps;
+        float m[2], l[2] = {0.f, 0.f}, z[2] = {0.f, 0.f}, o[kMine];
 #pragma unroll
-        for (int k = 0; k < kBufs; ++k)
-          m = fmaxf(m, buf[(k * C::kRegs + 32 + (h & 1)) * 32 + hl]);
-        const float r = ref_of(m);
-        float o = 0.f, l = 0.f, z = 0.f;
+        for (int i = 0; i < kMine; ++i) o[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          m[c] = kNone;
+#pragma unroll
+          for (int k = 0; k < kBufs; ++k)
+            m[c] = fmaxf(m[c], buf[(k * C::kRegs + 32 + c) * 32 + lane]);
+        }
 #pragma unroll
         for (int k = 0; k < kBufs; ++k) {
-          const float* bk = buf + k * C::kRegs * 32;
-          const float s = exp2_fast(bk[(32 + (h & 1)) * 32 + hl] - r);
-          float v = bk[reg * 32 + ln];
-          if constexpr (G < 8) v += bk[reg * 32 + ln + 2];
-          o = fmaf(s, v, o);
-          l = fmaf(s, bk[(34 + (h & 1)) * 32 + hl], l);
-          if constexpr (INT4) z = fmaf(s, bk[(36 + (h & 1)) * 32 + hl], z);
+          const float* bk = buf + k * C::kRegs * 32 + lane;
+          float s[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            s[c] = exp2_fast(bk[(32 + c) * 32] - m[c]);
+            l[c] = fmaf(s[c], bk[(34 + c) * 32], l[c]);
+            if constexpr (INT4) z[c] = fmaf(s[c], bk[(36 + c) * 32], z[c]);
+          }
+#pragma unroll
+          for (int i = 0; i < kMine; ++i)
+            o[i] = fmaf(s[i & 1], bk[(warp * kMine + i) * 32], o[i]);
         }
-        if constexpr (INT4) o = fmaf(o, 0x1p9f, z);
-        if (whole) {
-          const size_t row = (size_t)g.b * a.hq + g.kvh * G + h;
-          a.o[row * kHeadDim + d] = l == 0.f ? 0.f : o / l;
-          if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        } else {
-          part[h * kPartStride + d] = o;
-          if (d == 0) {
-            part[h * kPartStride + kHeadDim] = m;
-            part[h * kPartStride + kHeadDim + 1] = l;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int reg = warp * kMine + i, c = i & 1, h = 2 * lt + c;
+          float v = o[i];
+          if constexpr (G < 8) v += __shfl_xor_sync(0xffffffffu, v, 2);  // hi and lo parts
+          int d;
+          if constexpr (INT4) {
+            d = 16 * lg + (reg >> 2) * 2 + (reg >> 1 & 1);
+            v = fmaf(v, 0x1p9f, z[c]);
+          } else {
+            d = 16 * (reg >> 2) + 8 * (reg >> 1 & 1) + lg;
+          }
+          if (h < G) {
+            const size_t row = (size_t)g.b * a.hq + g.kvh * G + h;
+            if (whole) a.o[row * kHeadDim + d] = l[c] == 0.f ? 0.f : v / l[c];
+            else part[h * kPartStride + d] = v;
+          }
+        }
+        if (warp == 0 && lg == 0) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int h = 2 * lt + c;
+            if (h >= G) continue;
+            if (whole) {
+              a.lse[(size_t)g.b * a.hq + g.kvh * G + h] =
+                  l[c] == 0.f ? -INFINITY : (m[c] + log2f(l[c])) * kLn2;
+            } else {
+              part[h * kPartStride + kHeadDim] = m[c];
+              part[h * kPartStride + kHeadDim + 1] = l[c];
+            }
           }
         }
       }
@@ -618,17 +663,16 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
           __syncthreads();
           constexpr int kSub = kWarps / G;    // warps per head
           const int h = warp % G, sub = warp / G;
-          float m = -INFINITY;
+          float m = kNone;
           for (int c = lane; c < parts; c += 32) m = fmaxf(m, wt[c * G + h]);
           m = warp_max(m);
-          const float r = ref_of(m);
           float l = 0.f;
-          for (int c = lane; c < parts; c += 32) l = fmaf(exp2_fast(wt[c * G + h] - r), ls[c * G + h], l);
+          for (int c = lane; c < parts; c += 32) l = fmaf(exp2_fast(wt[c * G + h] - m), ls[c * G + h], l);
           l = warp_sum(l);
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
           for (int c = sub; c < parts; c += kSub) {
-            const float s = exp2_fast(wt[c * G + h] - r);
+            const float s = exp2_fast(wt[c * G + h] - m);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(at(c, h) + 4 * lane));
             o.x = fmaf(s, v.x, o.x), o.y = fmaf(s, v.y, o.y);
             o.z = fmaf(s, v.z, o.z), o.w = fmaf(s, v.w, o.w);

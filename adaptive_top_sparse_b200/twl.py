@@ -143,18 +143,25 @@ for _name, (_res, _args) in _sigs.items():
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_have_gpu = None
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        if torch.cuda.is_available():
-            return torch.cuda.current_stream().cuda_stream
-        return None
+        global _have_gpu
+        if _have_gpu is None:
+            _have_gpu = torch.cuda.is_available()
+        if not _have_gpu:
+            return None
+        if _raw_stream is not None:          # the handle alone, without a Stream object around it
+            return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -166,7 +173,7 @@ def _check(st: int, where: str) -> None:
 
 
 def _nbytes(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+    return 0 if t is None else t.nbytes
 
 
 @dataclass
@@ -190,9 +197,11 @@ class PagedKV:
         return int(self.page_table.shape[1])
 
     def c(self) -> _PagedKV:
-        return _PagedKV(_ptr(self.k), _ptr(self.v), _ptr(self.page_table), _ptr(self.seq_lens),
-                        self.batch, self.num_kv_heads, self.head_dim, self.page_size,
-                        self.max_pages, self.num_phys_pages)
+        table = self.page_table
+        batch, max_pages = table.shape
+        return _PagedKV(_ptr(self.k), _ptr(self.v), table.data_ptr(), _ptr(self.seq_lens),
+                        batch, self.num_kv_heads, self.head_dim, self.page_size, max_pages,
+                        self.num_phys_pages)
 
 
 def twl_status_string(status: int) -> str:
@@ -409,10 +418,12 @@ class Int4KV:
         return int(self.page_table.shape[1])
 
     def c(self) -> _Int4KV:
-        return _Int4KV(_ptr(self.k), _ptr(self.k_scale_zero), _ptr(self.v),
-                       _ptr(self.v_scale_zero), _ptr(self.page_table), _ptr(self.seq_lens),
-                       self.batch, self.num_kv_heads, self.head_dim, self.page_size,
-                       self.max_pages, self.num_phys_pages)
+        table = self.page_table
+        batch, max_pages = table.shape
+        return _Int4KV(self.k.data_ptr(), self.k_scale_zero.data_ptr(), self.v.data_ptr(),
+                       self.v_scale_zero.data_ptr(), table.data_ptr(), self.seq_lens.data_ptr(),
+                       batch, self.num_kv_heads, self.head_dim, self.page_size, max_pages,
+                       self.num_phys_pages)
 
 
 def twl_int4_decode(q, num_q_heads: int, kv: Int4KV, k_new, v_new, advance: bool, sinks: int,
@@ -425,7 +436,7 @@ def twl_int4_decode(q, num_q_heads: int, kv: Int4KV, k_new, v_new, advance: bool
 
 def _pools(pools):
     """The pools (tensors [P][...]) as an array of twl_page_pool."""
-    return (_PagePool * len(pools))(*[(_ptr(t), _nbytes(t) // t.shape[0]) for t in pools])
+    return (_PagePool * len(pools))(*[(t.data_ptr(), t.nbytes // t.shape[0]) for t in pools])
 
 
 def twl_remap_pages(pools, page_table, seq_lens, num_phys_pages: int, parent, reserve, sinks: int,
