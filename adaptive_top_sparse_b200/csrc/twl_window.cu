@@ -46,11 +46,11 @@ template <bool INT4>
 struct Cfg;
 template <>
 struct Cfg<false> {
-  static constexpr int kWarps = 8, kStages = 3, kTile = 8192, kRegs = 36;
+  static constexpr int kWarps = 8, kStages = 3, kPages = 1, kTile = 8192, kRegs = 36;
 };
 template <>
 struct Cfg<true> {
-  static constexpr int kWarps = 16, kStages = 5, kTile = 2176, kRegs = 38;
+  static constexpr int kWarps = 12, kStages = 3, kPages = 2, kTile = 4352, kRegs = 38;
 };
 
 template <bool INT4>
@@ -65,9 +65,10 @@ struct Group {
   int b, kvh, gs, ge;
   int n, lo;     // keys; first key of the window
   int sink_pages, first_page;  // sink pages before the window's first page
+  int pages;                   // of both kinds: kPages of them are a tile
 };
 
-__device__ __forceinline__ Group group_of(const Args& a, const int* prefix, int f) {
+__device__ __noinline__ Group group_of(const Args& a, const int* prefix, int f) {
   int x = 0, y = a.batch;  // prefix[x] * hkv <= f < prefix[y] * hkv
   while (y - x > 1) {
     const int mid = (x + y) >> 1;
@@ -84,12 +85,13 @@ __device__ __forceinline__ Group group_of(const Args& a, const int* prefix, int 
   g.lo = max(0, g.n - a.window);
   g.first_page = g.lo / kPage;
   g.sink_pages = min((min(a.sinks, g.n) + kPage - 1) / kPage, g.first_page);
+  g.pages = g.sink_pages + (g.n + kPage - 1) / kPage - g.first_page;
   return g;
 }
 
-// Tiles of sequence b per kv-head; 0 for an empty slot and for one that cannot be served (flagged
+// Visible pages of sequence b; 0 for an empty slot and for one that cannot be served (flagged
 // by `report`).
-__device__ int seq_tiles(const Args& a, int b, bool report) {
+__device__ int seq_pages(const Args& a, int b, bool report) {
   int n = a.seq_lens[b];
   if (a.appended) {
     const int j = n >> 4;
@@ -132,6 +134,20 @@ __device__ __forceinline__ float exp2_fast(float x) {
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+// 16 bytes at src + OFF to shared memory at dst + OFF.
+template <int OFF>
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;\n" ::"r"(dst), "l"(src),
+               "n"(OFF));
+}
+// The same, or 16 zeros when `hide`.
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool hide) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n"
+      " cp.async.cg.shared.global [%0], [%1], 16, p;\n}\n" ::"r"(dst), "l"(src),
+      "r"((uint32_t)hide));
 }
 
 // 16-byte slot of chunk c (0..3) of row r of a 4-bit V tile.  A lane reads 8 bytes of the rows of
@@ -217,12 +233,13 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
     k_window_decode(const __grid_constant__ Args a) {
   using C = Cfg<INT4>;
   constexpr int kWarps = C::kWarps, kStages = C::kStages, kTile = C::kTile, kBufs = kWarps / 2;
+  constexpr int kPages = C::kPages;
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* ring = smem;
   float* buf = reinterpret_cast<float*>(smem + (size_t)kWarps * kStages * kTile);
   int* prefix = reinterpret_cast<int*>(buf + kBufs * C::kRegs * 32);
   __shared__ int scan_sh[33];
-  __shared__ int tile_base[kWarps][kStages];  // first token of a stage's page, or -1: no page
+  __shared__ int tile_base[kWarps][kStages][kPages];  // first token of a stage's page; -1: none
   __shared__ int is_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -232,7 +249,7 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
   int carry = 0;
   for (int base = 0; base < a.batch; base += blockDim.x) {
     const int b = base + tid;
-    const int c = b < a.batch ? seq_tiles(a, b, blockIdx.x == 0) : 0;
+    const int c = b < a.batch ? (seq_pages(a, b, blockIdx.x == 0) + kPages - 1) / kPages : 0;
     int total;
     const int ex = block_exclusive_scan(c, scan_sh, &total);
     if (b < a.batch) prefix[b] = carry + ex;
@@ -258,61 +275,93 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
   if (run < runs) {
     const int f0 = (int)((long long)total * run / runs);
     const int f1 = (int)((long long)total * (run + 1) / runs);
-    unsigned char* my_ring = ring + (size_t)warp * kStages * kTile;
 
-    // ---- loads: tile lf goes to stage ls; its page id is fetched one tile ahead
+    // ---- loads: the warp's next tile lf goes to the ring's stage ls; its page id is fetched one
+    // tile ahead.  Addresses are running values: this is done for every 2 KB.
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring) + warp * kStages * kTile;
+    const uint8_t *k_lane, *v_lane;  // the lane's 16 bytes of row 0 (fp16: of row lane / 16)
+    const uint32_t* sz_lane = nullptr;
+    uint32_t k_to, v_to;             // where they go in a stage
+    if constexpr (INT4) {
+      k_lane = a.kc + lane * 16;
+      v_lane = a.vc + lane * 16;
+      sz_lane = (lane < 4 ? a.ksz : a.vsz) + 4 * (lane & 3);
+      k_to = lane * 16;
+      v_to = 1024 + v_slot(lane >> 2, lane & 3) * 16;
+    } else {
+      k_lane = reinterpret_cast<const uint8_t*>(a.k) + lane * 16;
+      v_lane = reinterpret_cast<const uint8_t*>(a.v) + lane * 16;
+    }
     int lf = f0 + warp, ls = 0;
-    Group lgp = group_of(a, prefix, min(lf, f1 - 1));
-    auto page_of = [&](const Group& g, int f) {
-      const int i = f - g.gs;
-      return i < g.sink_pages ? i : g.first_page + i - g.sink_pages;
+    int lgs, lend, lsink, lgap, lcount, lkvh, ln, llo;  // of the group of lf
+    const int* ltable;
+    auto enter = [&]() {
+      const Group g = group_of(a, prefix, lf);
+      lgs = g.gs;
+      lend = g.ge;
+      lsink = g.sink_pages;
+      lgap = g.first_page - g.sink_pages;
+      lcount = g.pages;
+      lkvh = g.kvh;
+      ln = g.n;
+      llo = g.lo;
+      ltable = a.page_table + (size_t)g.b * a.max_pages;
     };
-    auto fetch_phys = [&]() {
-      if (lf >= f1) return -1;
-      if (lf >= lgp.ge) lgp = group_of(a, prefix, lf);
-      return a.page_table[(size_t)lgp.b * a.max_pages + page_of(lgp, lf)];
+    int lpage[kPages], lphys[kPages];  // -1 as a page: behind the group's last
+    auto fetch = [&]() {
+      if (lf >= f1) return;
+      if (lf >= lend) enter();
+#pragma unroll
+      for (int h = 0; h < kPages; ++h) {
+        const int i = (lf - lgs) * kPages + h;
+        lpage[h] = i >= lcount ? -1 : i < lsink ? i : i + lgap;
+        lphys[h] = i < lcount ? ltable[lpage[h]] : -1;
+      }
     };
-    const int v_dst = 1024 + v_slot(lane >> 2, lane & 3) * 16;
-    const uint32_t* sz_src = (lane < 4 ? a.ksz : a.vsz) + 4 * (lane & 3);
-    int phys = fetch_phys();
+    if (lf < f1) enter(), fetch();
     auto issue = [&]() {
       if (lf < f1) {
-        const int base = page_of(lgp, lf) * kPage;
-        const bool ok = phys >= 0 && phys < a.num_phys;
+#pragma unroll
+        for (int h = 0; h < kPages; ++h) {
+        const bool ok = (unsigned)lphys[h] < (unsigned)a.num_phys;
         if (lane == 0) {
-          tile_base[warp][ls] = ok ? base : -1;
-          if (!ok) raise_flag(a.flags, TWL_FLAG_BAD_INDEX);
+          tile_base[warp][ls][h] = ok ? lpage[h] * kPage : -1;
+          if (!ok && lpage[h] >= 0) raise_flag(a.flags, TWL_FLAG_BAD_INDEX);
         }
-        unsigned char* st = my_ring + ls * kTile;
-        const size_t row0 = ok ? ((size_t)phys * a.hkv + lgp.kvh) * kPage : 0;
+        const uint32_t st = ring_at + ls * kTile + h * (kTile / kPages);
+        const uint32_t row0 = ok ? (uint32_t)(lphys[h] * a.hkv + lkvh) * kPage : 0u;
         if constexpr (INT4) {
-          const uint8_t* ks = a.kc + row0 * 64 + lane * 16;
-          const uint8_t* vs = a.vc + row0 * 64 + lane * 16;
-          cp_async16(st + lane * 16, ks, ok);
-          cp_async16(st + lane * 16 + 512, ks + 512, ok);
-          cp_async16(st + v_dst, vs, ok);
-          cp_async16(st + v_dst + 512, vs + 512, ok);  // rows r and r + 8 lie 512 bytes apart
-          if (lane < 8) cp_async16(st + 2048 + lane * 16, sz_src + row0, ok);
+          const uint8_t* ks = k_lane + (uint64_t)row0 * 64;
+          const uint8_t* vs = v_lane + (uint64_t)row0 * 64;
+          if (ok) {  // the codes of a page that is not there are not read
+            copy16<0>(st + k_to, ks);
+            copy16<512>(st + k_to, ks);
+            copy16<0>(st + v_to, vs);
+            copy16<512>(st + v_to, vs);  // rows r and r + 8 lie 512 bytes apart
+            if (lane < 8) copy16<0>(st + 2048 + lane * 16, sz_lane + row0);
+          }
         } else {
+          const uint8_t* ks = k_lane + (uint64_t)row0 * 256;
+          const uint8_t* vs = v_lane + (uint64_t)row0 * 256;
           const int c = lane & 15;
 #pragma unroll
           for (int it = 0; it < 8; ++it) {
-            const int r = it * 2 + (lane >> 4), tok = base + r;
+            const int r = it * 2 + (lane >> 4), tok = lpage[h] * kPage + r;
             // rows nobody sees are zeroed: a weight of 0 times a stale infinity would be NaN
-            const bool see = ok && tok < lgp.n && (tok < a.sinks || tok >= lgp.lo);
-            const size_t off = (row0 + r) * kHeadDim + c * 8;
-            const int slot = r * 256 + ((c ^ (r & 7)) * 16);
-            cp_async16(st + slot, a.k + off, see);
-            cp_async16(st + 4096 + slot, a.v + off, see);
+            const bool hide = !(ok && tok < ln && (tok < a.sinks || tok >= llo));
+            const uint32_t to = st + r * 256 + ((c ^ (r & 7)) * 16);
+            copy16_or_zero(to, ks + it * 512, hide);
+            copy16_or_zero(to + 4096, vs + it * 512, hide);
           }
         }
+        }
         lf += kWarps;
-        phys = fetch_phys();
+        fetch();
       }
       cp_async_commit();
       ls = ls + 1 == kStages ? 0 : ls + 1;
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) issue();
 
     int f = f0 + warp, cs = 0;
@@ -365,95 +414,121 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
         cp_async_wait<kStages - 2>();
         __syncwarp();  // every lane's copies have landed, and the stage read last is free
         issue();
-        unsigned char* tile = my_ring + cs * kTile;
-        const int base = tile_base[warp][cs];
+        unsigned char* tile = ring + (warp * kStages + cs) * kTile;
+        int base[kPages];
+        bool clear = true, any = false;
+#pragma unroll
+        for (int h = 0; h < kPages; ++h) {
+          base[h] = tile_base[warp][cs][h];
+          any = any || base[h] >= 0;
+          clear = clear && base[h] >= 0 && base[h] + kPage <= g.n &&
+                  (base[h] >= g.lo || base[h] + kPage <= a.sinks);
+        }
         cs = cs + 1 == kStages ? 0 : cs + 1;
-        if (base < 0) continue;
-        const bool clear = base + kPage <= g.n && (base >= g.lo || base + kPage <= a.sinks);
-        float x[4], w[4];
+        if (!any) continue;
+        float x[kPages][4], w[kPages][4];
+        auto sees = [&](int h, int r) {
+          const int key = base[h] + lg + 8 * r;
+          return base[h] >= 0 && key < g.n && (key < a.sinks || key >= g.lo);
+        };
         if constexpr (INT4) {
-          uint32_t* ksz = reinterpret_cast<uint32_t*>(tile + 2048);
-          uint32_t* vsz = ksz + 16;
-          if (a.appended && (unsigned)(g.n - 1 - base) < (unsigned)kPage) {
-            // the new token's row: quantised here, kept in the cache and patched into the tile
-            const int r = (g.n - 1) & (kPage - 1);
-            const int ph = a.page_table[(size_t)g.b * a.max_pages + base / kPage];
-            const size_t row = ((size_t)ph * a.hkv + g.kvh) * kPage + r;
-            const size_t in = ((size_t)g.b * a.hkv + g.kvh) * kHeadDim + lane * 4;
-            uint32_t sz;
-            uint16_t code = quantize_row_warp(load_half4(a.k_new + in), &sz);
-            reinterpret_cast<uint16_t*>(a.kc + row * 64)[lane] = code;
-            reinterpret_cast<uint16_t*>(tile + r * 64)[lane] = code;
-            if (lane == 0) a.ksz[row] = sz, ksz[r] = sz;
-            code = quantize_row_warp(load_half4(a.v_new + in), &sz);
-            reinterpret_cast<uint16_t*>(a.vc + row * 64)[lane] = code;
-            reinterpret_cast<uint16_t*>(tile + 1024 + v_slot(r, lane >> 3) * 16)[lane & 7] = code;
-            if (lane == 0) a.vsz[row] = sz, vsz[r] = sz;
-            __syncwarp();
-          }
-          // A 4-bit code c at bits 4-7 of a half is the fp16 value c 2^-20 (fp16 is linear in its
-          // bits up to 2^11).  Not at bits 0-3, where it is c 2^-24: the tensor core aligns products
-          // by exponent, and ten leading zeros of a subnormal cost the sum ten bits (measured: 6e-5
-          // instead of 1e-6 of max|v|).
-          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-          const uint4 ra = *reinterpret_cast<const uint4*>(tile + lg * 64 + lt * 16);
-          const uint4 rb = *reinterpret_cast<const uint4*>(tile + (lg + 8) * 64 + lt * 16);
-          const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+          float sv[kPages][2], zv[kPages][2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t a0[4] = {wa[i] << 4 & kNibble, wb[i] << 4 & kNibble,
-                                    wa[i] >> 4 & kNibble, wb[i] >> 4 & kNibble};
-            const uint32_t a1[4] = {wa[i] & kNibble, wb[i] & kNibble, wa[i] >> 8 & kNibble,
-                                    wb[i] >> 8 & kNibble};
-            mma_16816(s0, a0, qb[4 * i], qb[4 * i + 1]);
-            mma_16816(s1, a1, qb[4 * i + 2], qb[4 * i + 3]);
-          }
-          float sv[2], zv[2];
+          for (int h = 0; h < kPages; ++h) {
+            unsigned char* page = tile + h * 2176;
+            uint32_t* ksz = reinterpret_cast<uint32_t*>(page + 2048);
+            uint32_t* vsz = ksz + 16;
+            if (a.appended && base[h] >= 0 && (unsigned)(g.n - 1 - base[h]) < (unsigned)kPage) {
+              // the new token's row: quantised here, kept in the cache and patched into the tile
+              const int r = (g.n - 1) & (kPage - 1);
+              const int ph = a.page_table[(size_t)g.b * a.max_pages + base[h] / kPage];
+              const size_t row = ((size_t)ph * a.hkv + g.kvh) * kPage + r;
+              const size_t in = ((size_t)g.b * a.hkv + g.kvh) * kHeadDim + lane * 4;
+              uint32_t sz;
+              uint16_t code = quantize_row_warp(load_half4(a.k_new + in), &sz);
+              reinterpret_cast<uint16_t*>(a.kc + row * 64)[lane] = code;
+              reinterpret_cast<uint16_t*>(page + r * 64)[lane] = code;
+              if (lane == 0) a.ksz[row] = sz, ksz[r] = sz;
+              code = quantize_row_warp(load_half4(a.v_new + in), &sz);
+              reinterpret_cast<uint16_t*>(a.vc + row * 64)[lane] = code;
+              reinterpret_cast<uint16_t*>(page + 1024 + v_slot(r, lane >> 3) * 16)[lane & 7] = code;
+              if (lane == 0) a.vsz[row] = sz, vsz[r] = sz;
+              __syncwarp();
+            }
+            // A 4-bit code c at bits 4-7 of a half is the fp16 value c 2^-20 (fp16 is linear in its
+            // bits up to 2^11).  Not at bits 0-3, where it is c 2^-24: the tensor core aligns
+            // products by exponent, and ten leading zeros of a subnormal cost the sum ten bits
+            // (measured: 6e-5 instead of 1e-6 of max|v|).
+            float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint4 ra = *reinterpret_cast<const uint4*>(page + lg * 64 + lt * 16);
+            const uint4 rb = *reinterpret_cast<const uint4*>(page + (lg + 8) * 64 + lt * 16);
+            const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(ksz + lg + 8 * r));
-            const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(vsz + lg + 8 * r));
-            sv[r] = vf.x, zv[r] = fmaf(8.f, vf.x, vf.y);  // V's codes enter as c - 8
-            const float ks = kf.x * scale_k;
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a0[4] = {wa[i] << 4 & kNibble, wb[i] << 4 & kNibble,
+                                      wa[i] >> 4 & kNibble, wb[i] >> 4 & kNibble};
+              const uint32_t a1[4] = {wa[i] & kNibble, wb[i] & kNibble, wa[i] >> 8 & kNibble,
+                                      wb[i] >> 8 & kNibble};
+              mma_16816(s0, a0, qb[4 * i], qb[4 * i + 1]);
+              mma_16816(s1, a1, qb[4 * i + 2], qb[4 * i + 3]);
+            }
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-              x[2 * r + c] = fmaf(ks, s0[2 * r + c] + s1[2 * r + c], kf.y * qsum[c]);
+            for (int r = 0; r < 2; ++r) {
+              const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(ksz + lg + 8 * r));
+              const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(vsz + lg + 8 * r));
+              sv[h][r] = vf.x, zv[h][r] = fmaf(8.f, vf.x, vf.y);  // V's codes enter as c - 8
+              const float ks = kf.x * scale_k;
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                x[h][2 * r + c] = fmaf(ks, s0[2 * r + c] + s1[2 * r + c], kf.y * qsum[c]);
+            }
           }
           if (!clear) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const int key = base + lg + 8 * r;
-              if (!(key < g.n && (key < a.sinks || key >= g.lo))) {
-                x[2 * r] = x[2 * r + 1] = -INFINITY;
-                sv[r] = zv[r] = 0.f;
-              }
-            }
+            for (int h = 0; h < kPages; ++h)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                if (!sees(h, r)) {
+                  x[h][2 * r] = x[h][2 * r + 1] = -INFINITY;
+                  sv[h][r] = zv[h][r] = 0.f;
+                }
           }
           // The weight that meets V's codes is w = p s_v, so the reference m covers the score and
           // s_v's exponent: w then stays below 2^9, and its two fp16 parts keep 22 bits whatever
           // the scale of V.  Checked on the outcome: it is raised for few tiles.
-          float p[4];
+          float p[kPages][4];
           auto weigh = [&]() {
+            bool high = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              p[i] = exp2_fast(x[i] - st.m[i & 1]);
-              w[i] = p[i] * sv[i >> 1];
+            for (int h = 0; h < kPages; ++h) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                p[h][i] = exp2_fast(x[h][i] - st.m[i & 1]);
+                w[h][i] = p[h][i] * sv[h][i >> 1];
+              }
+              high = high || max4(w[h]) > 512.f || max4(p[h]) > 0x1p33f;
             }
+            return high;
           };
-          weigh();
-          if (__any_sync(0xffffffffu, max4(w) > 512.f || max4(p) > 0x1p33f)) {
-            float t[4];
+          if (__any_sync(0xffffffffu, weigh())) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              t[i] = x[i] + (float)max((int)(__float_as_uint(sv[i >> 1]) >> 23) - 127, -24);
-            raise_max(st, t);
+            for (int h = 0; h < kPages; ++h) {
+              float t[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                t[i] = x[h][i] +
+                       (float)max((int)(__float_as_uint(sv[h][i >> 1]) >> 23) - 127, -24);
+              raise_max(st, t);
+            }
             weigh();
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            st.l[i & 1] += p[i];
-            st.z[i & 1] = fmaf(p[i], zv[i >> 1], st.z[i & 1]);
-          }
+          for (int h = 0; h < kPages; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              st.l[i & 1] += p[h][i];
+              st.z[i & 1] = fmaf(p[h][i], zv[h][i >> 1], st.z[i & 1]);
+            }
         } else {
           float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
           const uint32_t kb = (uint32_t)__cvta_generic_to_shared(tile);
@@ -467,64 +542,66 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
             mma_16816(s1, fb, qb[2 * kk + 2], qb[2 * kk + 3]);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = (s0[i] + s1[i]) * a.scale_log2;
+          for (int i = 0; i < 4; ++i) x[0][i] = (s0[i] + s1[i]) * a.scale_log2;
           if (!clear) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const int key = base + lg + 8 * r;
-              if (!(key < g.n && (key < a.sinks || key >= g.lo)))
-                x[2 * r] = x[2 * r + 1] = -INFINITY;
-            }
+            for (int r = 0; r < 2; ++r)
+              if (!sees(0, r)) x[0][2 * r] = x[0][2 * r + 1] = -INFINITY;
           }
-          if (__any_sync(0xffffffffu, fmaxf(x[0], x[2]) > st.m[0] + kSlack ||
-                                          fmaxf(x[1], x[3]) > st.m[1] + kSlack))
-            raise_max(st, x);
+          if (__any_sync(0xffffffffu, fmaxf(x[0][0], x[0][2]) > st.m[0] + kSlack ||
+                                          fmaxf(x[0][1], x[0][3]) > st.m[1] + kSlack))
+            raise_max(st, x[0]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            w[i] = exp2_fast(x[i] - st.m[i & 1]);
-            st.l[i & 1] += w[i];
+            w[0][i] = exp2_fast(x[0][i] - st.m[i & 1]);
+            st.l[i & 1] += w[0][i];
           }
         }
-        uint32_t ph[2], pl[2];
-        p_fragments<G>(w, lt >= 2, ph, pl);
-        if constexpr (INT4) {
-          const int c = lg >> 1;  // 16-byte chunk of the lane's 16 channels
-          uint2 v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 2 * lt + (i & 1) + (i >> 1) * 8;
-            v[i] = *reinterpret_cast<const uint2*>(tile + 1024 + v_slot(r, c) * 16 + (lg & 1) * 8);
-          }
-          const uint32_t x4[4] = {__byte_perm(v[0].x, v[1].x, 0x5410),
-                                  __byte_perm(v[0].x, v[1].x, 0x7632),
-                                  __byte_perm(v[0].y, v[1].y, 0x5410),
-                                  __byte_perm(v[0].y, v[1].y, 0x7632)};
-          const uint32_t y4[4] = {__byte_perm(v[2].x, v[3].x, 0x5410),
-                                  __byte_perm(v[2].x, v[3].x, 0x7632),
-                                  __byte_perm(v[2].y, v[3].y, 0x5410),
-                                  __byte_perm(v[2].y, v[3].y, 0x7632)};
-          // Block i: row g = channel 16 g + 2 i, row g + 8 = 16 g + 2 i + 1.  The codes enter as
-          // (c - 8) 2^-9: without the offset the sum of codes and the sum of zeros are both far
-          // larger than a diffuse head's o, and their difference is not an fp32 result any more
-          // (measured at 8K tokens: 2e-5 of |o| off instead of 2e-6).
+        for (int h = 0; h < kPages; ++h) {
+          uint32_t ph[2], pl[2];
+          p_fragments<G>(w[h], lt >= 2, ph, pl);
+          if constexpr (INT4) {
+            const unsigned char* page = tile + h * 2176;
+            const int c = lg >> 1;  // 16-byte chunk of the lane's 16 channels
+            uint2 v[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t xx = i & 1 ? x4[i >> 1] >> 8 : x4[i >> 1];
-            const uint32_t yy = i & 1 ? y4[i >> 1] >> 8 : y4[i >> 1];
-            const uint32_t av[4] = {centre(xx & 0x000F000Fu, 0x1p15f), centre(xx & kNibble, 0x1p11f),
-                                    centre(yy & 0x000F000Fu, 0x1p15f), centre(yy & kNibble, 0x1p11f)};
-            mma_16816(st.acc[i], av, ph[0], ph[1]);
-            if constexpr (G == 8) mma_16816(st.acc[i], av, pl[0], pl[1]);
-          }
-        } else {
-          const uint32_t vb = (uint32_t)__cvta_generic_to_shared(tile) + 4096;
+            for (int i = 0; i < 4; ++i) {
+              const int r = 2 * lt + (i & 1) + (i >> 1) * 8;
+              v[i] = *reinterpret_cast<const uint2*>(page + 1024 + v_slot(r, c) * 16 + (lg & 1) * 8);
+            }
+            const uint32_t x4[4] = {__byte_perm(v[0].x, v[1].x, 0x5410),
+                                    __byte_perm(v[0].x, v[1].x, 0x7632),
+                                    __byte_perm(v[0].y, v[1].y, 0x5410),
+                                    __byte_perm(v[0].y, v[1].y, 0x7632)};
+            const uint32_t y4[4] = {__byte_perm(v[2].x, v[3].x, 0x5410),
+                                    __byte_perm(v[2].x, v[3].x, 0x7632),
+                                    __byte_perm(v[2].y, v[3].y, 0x5410),
+                                    __byte_perm(v[2].y, v[3].y, 0x7632)};
+            // Block i: row g = channel 16 g + 2 i, row g + 8 = 16 g + 2 i + 1.  The codes enter as
+            // (c - 8) 2^-9: without the offset the sum of codes and the sum of zeros are both far
+            // larger than a diffuse head's o, and their difference is not an fp32 result any more
+            // (measured at 8K tokens: 2e-5 of |o| off instead of 2e-6).
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = (lane >> 4) * 8 + (lane & 7);
-            uint32_t av[4];
-            ldmatrix4_trans(av, vb + r * 256 + (((2 * i + ((lane >> 3) & 1)) ^ (r & 7)) * 16));
-            mma_16816(st.acc[i], av, ph[0], ph[1]);
-            if constexpr (G == 8) mma_16816(st.acc[i], av, pl[0], pl[1]);
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t xx = i & 1 ? x4[i >> 1] >> 8 : x4[i >> 1];
+              const uint32_t yy = i & 1 ? y4[i >> 1] >> 8 : y4[i >> 1];
+              const uint32_t av[4] = {
+                  centre(xx & 0x000F000Fu, 0x1p15f), centre(xx & kNibble, 0x1p11f),
+                  centre(yy & 0x000F000Fu, 0x1p15f), centre(yy & kNibble, 0x1p11f)};
+              mma_16816(st.acc[i], av, ph[0], ph[1]);
+              if constexpr (G == 8) mma_16816(st.acc[i], av, pl[0], pl[1]);
+            }
+          } else {
+            const uint32_t vb = (uint32_t)__cvta_generic_to_shared(tile) + 4096;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = (lane >> 4) * 8 + (lane & 7);
+              uint32_t av[4];
+              ldmatrix4_trans(av, vb + r * 256 + (((2 * i + ((lane >> 3) & 1)) ^ (r & 7)) * 16));
+              mma_16816(st.acc[i], av, ph[0], ph[1]);
+              if constexpr (G == 8) mma_16816(st.acc[i], av, pl[0], pl[1]);
+            }
           }
         }
       }
@@ -577,7 +654,7 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
       float* part = a.part + ((size_t)run * 2 + (g.gs < f0 ? 0 : 1)) * G * kPartStride;
       {
         // every warp joins 32 / kWarps of the accumulators, each lane its own columns
-        constexpr int kMine = 32 / kWarps;
+        constexpr int kMine = (32 + kWarps - 1) / kWarps;
         float m[2], l[2] = {0.f, 0.f}, z[2] = {0.f, 0.f}, o[kMine];
 #pragma unroll
         for (int i = 0; i < kMine; ++i) o[i] = 0.f;
@@ -599,24 +676,27 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
             if constexpr (INT4) z[c] = fmaf(s[c], bk[(36 + c) * 32], z[c]);
           }
 #pragma unroll
-          for (int i = 0; i < kMine; ++i)
-            o[i] = fmaf(s[i & 1], bk[(warp * kMine + i) * 32], o[i]);
+          for (int i = 0; i < kMine; ++i) {
+            const int reg = warp * kMine + i;
+            if (reg < 32) o[i] = fmaf(reg & 1 ? s[1] : s[0], bk[reg * 32], o[i]);
+          }
         }
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-          const int reg = warp * kMine + i, c = i & 1, h = 2 * lt + c;
+          const int reg = warp * kMine + i, c = reg & 1, h = 2 * lt + c;
+          const float zc = c ? z[1] : z[0], lc = c ? l[1] : l[0];
           float v = o[i];
           if constexpr (G < 8) v += __shfl_xor_sync(0xffffffffu, v, 2);  // hi and lo parts
           int d;
           if constexpr (INT4) {
             d = 16 * lg + (reg >> 2) * 2 + (reg >> 1 & 1);
-            v = fmaf(v, 0x1p9f, z[c]);
+            v = fmaf(v, 0x1p9f, zc);
           } else {
             d = 16 * (reg >> 2) + 8 * (reg >> 1 & 1) + lg;
           }
-          if (h < G) {
+          if (h < G && reg < 32) {
             const size_t row = (size_t)g.b * a.hq + g.kvh * G + h;
-            if (whole) a.o[row * kHeadDim + d] = l[c] == 0.f ? 0.f : v / l[c];
+            if (whole) a.o[row * kHeadDim + d] = lc == 0.f ? 0.f : v / lc;
             else part[h * kPartStride + d] = v;
           }
         }
@@ -671,7 +751,7 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
           l = warp_sum(l);
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-          for (int c = sub; c < parts; c += kSub) {
+          for (int c = sub; sub < kSub && c < parts; c += kSub) {
             const float s = exp2_fast(wt[c * G + h] - m);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(at(c, h) + 4 * lane));
             o.x = fmaf(s, v.x, o.x), o.y = fmaf(s, v.y, o.y);
