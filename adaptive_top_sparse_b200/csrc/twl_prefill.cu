@@ -113,6 +113,9 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                        uint64_t* bar) {
   asm volatile(
@@ -320,6 +323,19 @@ __device__ __forceinline__ Span span_of(const Args& a, const Chunk& c, int i0, i
   return s;
 }
 
+// Where run i of `runs` starts in a list of `total`.
+__device__ __forceinline__ long long cut_at(long long total, int i, int runs) {
+  if (total < (1 << 20)) return (unsigned)total * (unsigned)i / (unsigned)runs;  // far cheaper
+  return total * i / runs;
+}
+
+// The run that holds tile f.
+__device__ __forceinline__ int run_of(long long f, long long total, int runs) {
+  if (total < (1 << 20))
+    return (int)((((unsigned)f + 1u) * (unsigned)runs - 1u) / (unsigned)total);
+  return (int)(((f + 1) * runs - 1) / total);
+}
+
 // Every role walks the CTA's run of the list by itself: segments of units, in order.
 template <int G>
 struct Walk {
@@ -381,6 +397,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kQueries = kRows / G;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+  if (tid == kLoadWarp * 32) {
+    sm.aborted = 0;
+    bar_init(&sm.q_full, 1);
+    bar_init(&sm.q_free, 1);
+    for (int i = 0; i < kBufs; ++i) bar_init(&sm.full[i], 1), bar_init(&sm.empty[i], 2);
+    for (int x = 0; x < 2; ++x) {
+      bar_init(&sm.s_full[x], 1);
+      bar_init(&sm.p_full[x], 8);
+      bar_init(&sm.o_full[x], 1);
+      bar_init(&sm.o_free[x], 8);
+    }
+    for (int i = 0; i < kBufs; ++i) bar_init(&sm.v_ready[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_map(&qmap);
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     sptr(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
   // ---- prefix[b] = key tiles per kv-head of the sequences before b
   for (int b = warp; b < a.batch; b += kThreads / 32) {
     const Chunk c = chunk_of(a, b, blockIdx.x == 0 && lane == 0);
@@ -411,8 +449,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long total = prefix[a.batch] * a.hkv;
   const int runs = (int)min((long long)gridDim.x, total);
   const int run = blockIdx.x;
-  if (run >= runs) return;
-  const long long f0 = total * run / runs, f1 = total * (run + 1) / runs;
+  if (run >= runs) {
+    __syncthreads();  // the allocation is there
+    if (warp == kMmaWarp)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem));
+    return;
+  }
+  const long long f0 = cut_at(total, run, runs), f1 = cut_at(total, run + 1, runs);
   if (warp == 0) {
     int x = 0, y = a.batch;  // prefix[x] hkv <= f0 < prefix[y] hkv
     while (y - x > 1) {
@@ -445,25 +488,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       rest -= __shfl_sync(0xffffffffu, sum, 31);
       if (q0 * kQueries >= c.qn) break;  // not reached: rest is below the sum of all units
     }
-  }
-  if (tid == 0) {
-    sm.aborted = 0;
-    bar_init(&sm.q_full, 1);
-    bar_init(&sm.q_free, 1);
-    for (int i = 0; i < kBufs; ++i) bar_init(&sm.full[i], 1), bar_init(&sm.empty[i], 2);
-    for (int x = 0; x < 2; ++x) {
-      bar_init(&sm.s_full[x], 1);
-      bar_init(&sm.p_full[x], 8);
-      bar_init(&sm.o_full[x], 1);
-      bar_init(&sm.o_free[x], 8);
-    }
-    for (int i = 0; i < kBufs; ++i) bar_init(&sm.v_ready[i], 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  if (warp == kMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     sptr(&sm.tmem)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   fence_before();
   // the prefix lay where TMA writes next
@@ -552,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const uint64_t dq = smem_desc(sptr(qbuf), 16, 1024), dk = smem_desc(sptr(ring), 16, 1024),
                      dv = smem_desc(sptr(ring), 16384, 1024);
-      auto scores = [&](int x, int b) {
-        const uint64_t a0 = dq + (uint64_t)(x * (32768 >> 4)),
+      auto scores = [&](int x, int b, bool second) {
+        const uint64_t a0 = dq + (second ? 32768u >> 4 : 0u),
                        b0 = dk + (uint64_t)(b * (kBufBytes >> 4));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -562,53 +586,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mma_commit(&sm.s_full[x]);
       };
+      auto product = [&](int x, int vb, bool first) {  // O_x += P_x V, waits for the weights
+        if (first && units[x] > 0) {
+          wait(&sm.o_free[x], free_ph >> x & 1);
+          free_ph ^= 1u << x;
+        }
+        wait(&sm.p_full[x], p_ph >> x & 1);
+        p_ph ^= 1u << x;
+        if (!ok) return;
+        fence_after();
+        const uint64_t v0 = dv + (uint64_t)(vb * (kBufBytes >> 4));
+        // the weights of columns 64 .. lie over those columns' scores
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts(tmem + 256 + x * 128, tmem + x * 128 + (k >> 2) * 64 + (k & 3) * 8,
+                 v0 + k * (2048 >> 4), !first || k > 0);
+      };
       while (ok && w.next()) {
-        const bool two = w.two;
         wait(&sm.q_full, q_ph);
         q_ph ^= 1;
         wait_k(kb);
         if (!ok) break;
         fence_after();
-        scores(0, kb);
-        if (two) scores(1, kb);
-        mma_commit(&sm.empty[kb]);
-        if (w.tiles == 1) mma_commit(&sm.q_free);
-        wait_v(next_buf(kb));
-        for (int i = w.tiles; i > 0 && ok; --i) {
-          const int vb = next_buf(kb), kn = next_buf(vb);
-          const uint64_t v0 = dv + (uint64_t)(vb * (kBufBytes >> 4));
+        scores(0, kb, false);
+        if (w.two) {
+          // two query tiles, every key tile for both
+          scores(1, kb, true);
+          mma_commit(&sm.empty[kb]);
+          if (w.tiles == 1) mma_commit(&sm.q_free);
+          wait_v(next_buf(kb));
+          for (int i = w.tiles; i > 0 && ok; --i) {
+            const int vb = next_buf(kb), kn = next_buf(vb);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (x == 1 && !two) break;
-            if (i == w.tiles && units[x] > 0) {
-              wait(&sm.o_free[x], free_ph >> x & 1);
-              free_ph ^= 1u << x;
+            for (int x = 0; x < 2; ++x) {
+              product(x, vb, i == w.tiles);
+              if (!ok) break;
+              if (x == 1) mma_commit(&sm.empty[vb]);
+              if (i == 1) {
+                mma_commit(&sm.o_full[x]);
+                ++units[x];
+              } else {
+                if (x == 0) wait_k(kn);
+                else wait_v(next_buf(kn));
+                if (!ok) break;
+                scores(x, kn, x == 1);
+              }
             }
-            wait(&sm.p_full[x], p_ph >> x & 1);
-            p_ph ^= 1u << x;
             if (!ok) break;
-            fence_after();
-            // the weights of columns 64 .. lie over those columns' scores
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + (k >> 2) * 64 + (k & 3) * 8,
-                     v0 + k * (2048 >> 4), i < w.tiles || k > 0);
-            const bool last = x == 1 || !two;  // query tile
-            if (last) mma_commit(&sm.empty[vb]);
-            if (i == 1) {
+            if (i > 1) mma_commit(&sm.empty[kn]);
+            if (i == 2) mma_commit(&sm.q_free);
+            kb = kn;
+          }
+        } else {
+          // one query tile: even key tiles go through side 0 of TMEM, odd ones through side 1
+          mma_commit(&sm.empty[kb]);
+          if (w.tiles > 1) {
+            const int k1 = next_buf(next_buf(kb));
+            wait_k(k1);
+            if (!ok) break;
+            scores(1, k1, false);
+            mma_commit(&sm.empty[k1]);
+          }
+          if (w.tiles <= 2) mma_commit(&sm.q_free);
+          for (int j = 0; j < w.tiles && ok; ++j) {
+            const int x = j & 1, vb = next_buf(kb), kn = next_buf(vb);
+            wait_v(vb);
+            product(x, vb, j < 2);
+            if (!ok) break;
+            mma_commit(&sm.empty[vb]);
+            if (j + 2 >= w.tiles) {
               mma_commit(&sm.o_full[x]);
               ++units[x];
             } else {
-              if (x == 0) wait_k(kn);
-              if (last) wait_v(next_buf(kn));
+              const int k2 = next_buf(next_buf(kn));
+              wait_k(k2);
               if (!ok) break;
-              scores(x, kn);
+              scores(x, k2, false);
+              mma_commit(&sm.empty[k2]);
+              if (j + 3 == w.tiles) mma_commit(&sm.q_free);
             }
+            kb = kn;
           }
-          if (!ok) break;
-          if (i > 1) mma_commit(&sm.empty[kn]);
-          if (i == 2) mma_commit(&sm.q_free);
-          kb = kn;
         }
       }
     }
@@ -662,19 +720,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t sph = 0, oph = 0;
     uint32_t ntile = 0;  // key tiles so far, of the CTA
     while (w.next()) {
-      const int i = w.i0 + (x * kTileRows + row) / G;  // the row's query
+      // one query tile: side x of TMEM has every second key tile of the same rows
+      const int xq = w.two ? x : 0, step = w.two ? 1 : 2, first_tile = w.two ? 0 : x;
+      const int i = w.i0 + (xq * kTileRows + row) / G;  // the row's query
       const int t = w.c.n - w.c.qn + i;
-      const bool active = x == 0 || w.two;
+      const bool active = first_tile < w.tiles;
       const bool valid = i < w.c.qn;
-      if (!active) ntile += w.tiles;
       float m = -INFINITY, l = 0.f;
       // first and last query of this tile of rows: tiles of keys that all of them see need no mask
-      const int ta = w.s.t0 + x * (kTileRows / G), tb = min(ta + kTileRows / G, w.c.n) - 1;
-      for (int j = 0; active && j < w.tiles; ++j) {
+      const int ta = w.s.t0 + xq * (kTileRows / G), tb = min(ta + kTileRows / G, w.c.n) - 1;
+      for (int j = first_tile; j < w.tiles; j += step) {
         const bool live = warp_wait(sm, &sm.s_full[x], sph, a.flags);
         sph ^= 1;
         fence_after();
-        const int rec = sm.rec[ntile++ % kRecs], base = (rec >> 8) * kKeys, pages = rec & 0xFF;
+        const int rec = sm.rec[(ntile + j) % kRecs], base = (rec >> 8) * kKeys, pages = rec & 0xFF;
         const bool clear = pages == 0xFF && base + kKeys - 1 <= ta &&
                            (base > tb - a.window || base + kKeys <= a.sinks);
         // The columns are read twice, for their maximum and for their weights, and the weights' loop
@@ -731,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = exp2_fast(m - ref_of(mn));
           m = mn;
           l *= f;
-          if (j > 0) {  // this tile's scores were issued behind the last product into O
+          if (j != first_tile) {  // this tile's scores were issued behind the last product into O
 #pragma unroll 1
             for (int c = 0; c < 64; c += 16) {
               uint32_t o[16];
@@ -769,6 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) bar_arrive(&sm.p_full[x]);
       }
+      ntile += w.tiles;
       // ---- the unit's rows
       *mine = l;
       named_sync(pair_bar, 64);
@@ -780,6 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t out = (size_t)(w.c.qs + i) * a.hq + w.kvh * G + row % G;
       float* part = a.part + ((size_t)run * 2 + (w.tile0 > 0 ? 0 : 1)) * kPartFloats;
       const int prow = x * kTileRows + row;
+      const bool direct = w.whole && (w.two || w.tiles == 1);  // nothing to merge
       if (active && fine) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -788,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(o, to + 32 * c);
           wait_ld();
           keep_ld(o);
-          if (valid && w.whole) {
+          if (valid && direct) {
             uint32_t h[16];
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
@@ -811,44 +872,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(&sm.o_free[x]);
-        if (valid && w.whole && half == 0)
+        if (valid && direct && half == 0)
           a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        if (valid && !w.whole && half == 0) {
-          part[kRows * kHeadDim + prow] = m;
-          part[kRows * (kHeadDim + 1) + prow] = l;
-        }
       }
-      if (w.whole) continue;
+      if (direct) continue;
+      if (valid && half == 0) {  // a side without a tile has seen nothing
+        part[kRows * kHeadDim + prow] = active ? m : -INFINITY;
+        part[kRows * (kHeadDim + 1) + prow] = active ? l : 0.f;
+      }
       // ---- a cut unit: the run that arrives last merges the partials, in run order
       const long long fs = w.at - w.tiles - w.tile0;  // the unit's first tile in the list
-      const int first = (int)(((fs + 1) * runs - 1) / total);
-      const int last = (int)(((fs + w.s.tiles) * runs - 1) / total);
+      const int first = run_of(fs, total, runs), last = run_of(fs + w.s.tiles - 1, total, runs);
       __threadfence();
       named_sync(1, 512);
       if (tid == 0)
-        sm.is_last = !dead() && atomicAdd(a.done + first, 1u) == (unsigned)(last - first);
+        sm.is_last = !dead() && (first == last ||
+                                 atomicAdd(a.done + first, 1u) == (unsigned)(last - first));
       named_sync(1, 512);
       if (sm.is_last) {
         __threadfence();
         const int rows = min(kRows, (w.c.qn - w.i0) * G);
-        auto at = [&](int r) {  // the unit starts in run `first`: its second slot
-          return a.part + ((size_t)r * 2 + (r == first ? 1 : 0)) * kPartFloats;
+        const int sides = w.two ? 1 : 2;  // partials of a row in each run
+        auto at = [&](int k) {  // the unit starts in run `first`: its second slot
+          const int r = first + (k >> (sides - 1));
+          return a.part + ((size_t)r * 2 + (r == first ? 1 : 0)) * kPartFloats +
+                 (k & (sides - 1)) * kTileRows;
         };
+        auto o_at = [&](int k) {
+          const int r = first + (k >> (sides - 1));
+          return reinterpret_cast<const float4*>(
+                     a.part + ((size_t)r * 2 + (r == first ? 1 : 0)) * kPartFloats) +
+                 (k & (sides - 1)) * kTileRows;
+        };
+        const int parts = (last - first + 1) * sides;
         for (int e = tid; e < rows * 32; e += 512) {
           const int r = e % rows, c = e / rows;
           float mm = -INFINITY;
-          for (int k = first; k <= last; ++k) mm = fmaxf(mm, __ldcg(at(k) + kRows * kHeadDim + r));
+#pragma unroll 4
+          for (int k = 0; k < parts; ++k) mm = fmaxf(mm, __ldcg(at(k) + kRows * kHeadDim + r));
           const float ref = ref_of(mm);
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
           float ll = 0.f;
 #pragma unroll 4
-          for (int k = first; k <= last; ++k) {
-            const float* p = at(k);
-            const float f = exp2_fast(__ldcg(p + kRows * kHeadDim + r) - ref);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + c * kRows + r);
-            ll = fmaf(f, __ldcg(p + kRows * (kHeadDim + 1) + r), ll);
-            o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
-            o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+          for (int k = 0; k < parts; ++k) {
+            const float mk = __ldcg(at(k) + kRows * kHeadDim + r);
+            const float4 v = __ldcg(o_at(k) + c * kRows + r);
+            const float f = exp2_fast(mk - ref);
+            ll = fmaf(f, __ldcg(at(k) + kRows * (kHeadDim + 1) + r), ll);
+            if (mk != -INFINITY) {  // else nothing was written beside it
+              o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
+              o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+            }
           }
           const float inv = ll == 0.f ? 0.f : 1.f / ll;
           const size_t dst = (size_t)(w.c.qs + w.i0 + r / G) * a.hq + w.kvh * G + r % G;
@@ -857,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          pack_half2(__float2half_rn(o.z * inv), __float2half_rn(o.w * inv)));
           if (c == 0) a.lse[dst] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
         }
-        if (tid == 0) a.done[first] = 0u;
+        if (tid == 0 && first != last) a.done[first] = 0u;
       }
       named_sync(1, 512);
     }
