@@ -13,8 +13,8 @@
 // use the card as well as one long prompt, and lengths stay on the device.
 //
 // One CTA: nineteen warps.
-//   loader     TMA of the queries and of K and V pages (16 rows of 128 bytes a copy, 128-byte
-//              swizzle) into a ring of five 32 KB buffers
+//   loader     TMA of the queries and of K and V pages (a copy per page, 128-byte swizzle) into a
+//              ring of five 32 KB buffers
 //   fixer      zeroes the V rows nobody in the unit sees (a weight of 0 times a stale infinity
 //              would be NaN); only tiles at the edge of what is seen need it
 //   mma        one thread: S_x = Q_x K^T (tcgen05, fp16 in, fp32 in TMEM) and O_x += P_x V with P
@@ -116,11 +116,13 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                       uint64_t* bar) {
+// A page of one kv-head, coordinate y = its first row / 8: see the maps in launch_g.
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int y,
+                                         uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(sptr(bar)) : "memory");
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %2, %2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(0), "r"(y), "r"(sptr(bar))
+      : "memory");
 }
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
                                        uint64_t* bar) {
@@ -522,8 +524,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             phys = load_phys(a.page_table, w.b, p0 / kPage, a.max_pages, a.num_phys, a.flags);
         }
         const unsigned pages = __ballot_sync(0xffffffffu, phys >= 0);
-        const int row = (__shfl_sync(0xffffffffu, phys, (lane & 15) >> 1) * a.hkv + w.kvh) * kPage;
-        const bool mine = pages >> ((lane & 15) >> 1) & 1;
         for (int kv = 0; kv < 2; ++kv, ++fill) {
           const int buf = fill % kBufs, round = fill / kBufs;
           if (round > 0 && !warp_wait(sm, &sm.empty[buf], (round - 1) & 1, a.flags)) {
@@ -535,9 +535,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_expect(&sm.full[buf], __popc(pages) * 4096);
           }
           __syncwarp();
-          if (lane < 16 && mine)
-            tma_2d(sptr(ring) + buf * kBufBytes + (lane & 1) * 16384 + (lane >> 1) * 2048,
-                   kv == 0 ? &kmap : &vmap, 64 * (lane & 1), row, &sm.full[buf]);
+          if (phys >= 0)
+            tma_page(sptr(ring) + buf * kBufBytes + lane * 4096, kv == 0 ? &kmap : &vmap,
+                     (phys * a.hkv + w.kvh) * (kPage / 8), &sm.full[buf]);
         }
         if (!ok) break;
       }
@@ -574,15 +574,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ready_ph ^= 1u << b;
         full_ph ^= 1u << b;
       };
-      const uint64_t dq = smem_desc(sptr(qbuf), 16, 1024), dk = smem_desc(sptr(ring), 16, 1024),
-                     dv = smem_desc(sptr(ring), 16384, 1024);
+      // key tiles: 16 groups of 8 rows, the two 64-column halves of a group behind one another
+      const uint64_t dq = smem_desc(sptr(qbuf), 16, 1024), dk = smem_desc(sptr(ring), 16, 2048),
+                     dv = smem_desc(sptr(ring), 1024, 2048);
       auto scores = [&](int x, int b, bool second) {
         const uint64_t a0 = dq + (second ? 32768u >> 4 : 0u),
                        b0 = dk + (uint64_t)(b * (kBufBytes >> 4));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint64_t off = (k >> 2) * (16384 >> 4) + (k & 3) * (32 >> 4);
-          mma_ss(tmem + x * 128, a0 + off, b0 + off, k > 0);
+          const uint64_t in = (k & 3) * (32 >> 4);
+          mma_ss(tmem + x * 128, a0 + (k >> 2) * (16384 >> 4) + in, b0 + (k >> 2) * (1024 >> 4) + in,
+                 k > 0);
         }
         mma_commit(&sm.s_full[x]);
       };
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           mma_ts(tmem + 256 + x * 128, tmem + x * 128 + (k >> 2) * 64 + (k & 3) * 8,
-                 v0 + k * (2048 >> 4), !first || k > 0);
+                 v0 + k * (4096 >> 4), !first || k > 0);
       };
       while (ok && w.next()) {
         wait(&sm.q_full, q_ph);
@@ -688,12 +690,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               const bool seen = key <= w.s.t1 && (key < a.sinks || key >= w.s.lo) &&
                                 (pages >> (r / kPage) & 1);
               if (!seen) {
-                unsigned char* p = ring + buf * kBufBytes + r * 128;
+                unsigned char* p = ring + buf * kBufBytes + (r >> 3) * 2048 + (r & 7) * 128;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                   const int cc = ((c + lane) & 7) * 16;
                   *reinterpret_cast<uint4*>(p + cc) = make_uint4(0, 0, 0, 0);
-                  *reinterpret_cast<uint4*>(p + 16384 + cc) = make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4*>(p + 1024 + cc) = make_uint4(0, 0, 0, 0);
                 }
               }
             }
@@ -963,7 +965,7 @@ EncodeFn encode_fn() {
 // Rows of 128 fp16 values in boxes of 64 columns (one 128-byte swizzle row).
 bool encode(CUtensorMap* map, const uint16_t* base, int rank, const cuuint64_t* dims,
             const cuuint64_t* strides, const cuuint32_t* box) {
-  const cuuint32_t ones[3] = {1, 1, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
   return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<uint16_t*>(base), dims,
                      strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -976,11 +978,14 @@ cudaError_t launch_g(const Args& a, cudaStream_t s) {
   const cuuint64_t qd[3] = {kHeadDim, (cuuint64_t)a.hq, (cuuint64_t)a.total_q};
   const cuuint64_t qst[2] = {kHeadDim * 2, (cuuint64_t)a.hq * kHeadDim * 2};
   const cuuint32_t qbox[3] = {64, G, kTileRows / G};
-  const cuuint64_t kd[2] = {kHeadDim, (cuuint64_t)a.num_phys * a.hkv * kPage};
-  const cuuint64_t kst[1] = {kHeadDim * 2};
-  const cuuint32_t kbox[2] = {64, kPage};
-  if (!encode_fn() || !encode(&qm, a.q, 3, qd, qst, qbox) || !encode(&km, a.k, 2, kd, kst, kbox) ||
-      !encode(&vm, a.v, 2, kd, kst, kbox))
+  // Keys: a page is one copy of 8 rows x 64 columns, both halves of the columns, both groups of 8
+  // rows, so that the groups of a key tile lie 2 KB apart whatever pages they come from (a copy per
+  // page and half took 75 cycles each: 1200 a tile of K or V instead of 800).
+  const cuuint64_t kd[4] = {64, 8, 2, (cuuint64_t)a.num_phys * a.hkv * (kPage / 8)};
+  const cuuint64_t kst[3] = {kHeadDim * 2, 128, 8 * kHeadDim * 2};
+  const cuuint32_t kbox[4] = {64, 8, 2, 2};
+  if (!encode_fn() || !encode(&qm, a.q, 3, qd, qst, qbox) || !encode(&km, a.k, 4, kd, kst, kbox) ||
+      !encode(&vm, a.v, 4, kd, kst, kbox))
     return cudaErrorNotSupported;
   cudaError_t e = cudaFuncSetAttribute(k_window_prefill<G>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
