@@ -12,11 +12,13 @@
 // the CTA arriving last merges in run order.  So a few long sequences with a handful of queries
 // use the card as well as one long prompt, and lengths stay on the device.
 //
-// One CTA: nineteen warps.
+// One CTA: twenty warps.
 //   loader     TMA of the queries and of K and V pages (a copy per page, 128-byte swizzle) into a
 //              ring of five 32 KB buffers
-//   fixer      zeroes the V rows nobody in the unit sees (a weight of 0 times a stale infinity
-//              would be NaN); only tiles at the edge of what is seen need it
+//   fixers     two warps that zero the V rows nobody in the unit sees: a weight of 0 times a stale
+//              infinity would be NaN.  A value that is not finite in a row which only some of the queries see is
+//              zeroed too and noted, and the queries that see it get their NaN at the end.  Only
+//              tiles at the edge of what is seen need either
 //   mma        one thread: S_x = Q_x K^T (tcgen05, fp16 in, fp32 in TMEM) and O_x += P_x V with P
 //              in TMEM over S and V taken as it lies in the page (MN-major)
 //   softmax x  eight warps per query tile, two threads per row: scores from TMEM, maximum, weights
@@ -38,13 +40,20 @@ namespace {
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kSlack = 8.f;  // log2: a row's maximum is raised only when exceeded by more
 constexpr int kRows = 256, kTileRows = 128, kKeys = 128;
-constexpr int kThreads = 608;
+constexpr int kThreads = 640;
 constexpr int kBufBytes = 32768, kBufs = 5;
 constexpr int kQBytes = 65536;
 constexpr int kRecs = 8;
+constexpr int kSpoils = 16, kSpoilsPer = 4;  // of the CTA's last segments; of one (two a fixer)
 constexpr int kMmaWarp = 16, kLoadWarp = 17, kFixWarp = 18;
 // partial of a cut unit: o as [32][256] float4 (column group, row), then max[256], sum[256]
 constexpr int kPartFloats = kRows * 130;
+
+// A value of V that is not finite, in a row that some of a unit's queries see and others do not.
+struct Spoil {
+  int seg, key;       // the CTA's segment; the row's position
+  uint32_t cols[4];   // its columns that are not finite
+};
 
 struct Smem {
   // barriers
@@ -56,6 +65,8 @@ struct Smem {
   int aborted;
   int rec[kRecs];  // of a key tile: pages that were loaded (bit per page), its number << 8
   int is_last;
+  uint32_t spoils;        // whether any segment so far has one
+  Spoil spoil[kSpoils];   // segment s: at kSpoilsPer (s % 4)
   // where the run starts
   int b, kvh, qt, tile;
   float swap[2][2][kTileRows];  // maxima and sums of the halves of the rows
@@ -325,6 +336,56 @@ __device__ __forceinline__ Span span_of(const Args& a, const Chunk& c, int i0, i
   return s;
 }
 
+// Which of two fp16 values are not finite (bits 0 and 1), and the two with 0 in place of those.
+__device__ __forceinline__ uint32_t odd_values(uint32_t x) {
+  return ((x & 0x7C00u) == 0x7C00u ? 1u : 0u) | ((x & 0x7C000000u) == 0x7C000000u ? 2u : 0u);
+}
+__device__ __forceinline__ uint32_t keep_finite(uint32_t x) {
+  const uint32_t b = odd_values(x);
+  return (b & 1 ? 0u : x & 0xFFFFu) | (b & 2 ? 0u : x & 0xFFFF0000u);
+}
+
+// A fixer warp: zeroes what is not finite in its 64 rows of a V tile (the first at position key0)
+// and notes the rows and columns for segment seg.  A warp has room for two rows of a segment;
+// further ones go to its second, under the lower of their positions.
+__device__ __noinline__ void spoilt_rows(Smem& s, unsigned char* v, int key0, int seg, int half) {
+  const int lane = threadIdx.x & 31;
+  Spoil* of = s.spoil + (seg % (kSpoils / kSpoilsPer)) * kSpoilsPer + 2 * half;
+#pragma unroll 1
+  for (int it = 0; it < 32; ++it) {
+    // 512 bytes: 4 rows of one half of the columns, chunks of 8 columns swizzled by row
+    const int r = (it >> 2) * 8 + (it & 1) * 4 + (lane >> 3);
+    uint4* at = reinterpret_cast<uint4*>(v + it * 512 + lane * 16);
+    const uint4 x = *at;
+    const uint32_t bad = odd_values(x.x) | odd_values(x.y) << 2 | odd_values(x.z) << 4 |
+                         odd_values(x.w) << 6;
+    if (bad)
+      *at = make_uint4(keep_finite(x.x), keep_finite(x.y), keep_finite(x.z), keep_finite(x.w));
+    const int col = (it >> 1 & 1) * 64 + (((lane & 7) ^ (r & 7)) * 8);
+    for (unsigned who = __ballot_sync(0xffffffffu, bad != 0); who; who &= who - 1) {
+      const int l = __ffs(who) - 1;
+      const uint32_t m = __shfl_sync(0xffffffffu, bad, l);
+      const int c = __shfl_sync(0xffffffffu, col, l), key = key0 + __shfl_sync(0xffffffffu, r, l);
+      if (lane != 0) continue;
+      for (int i = 0; i < 2; ++i) {
+        const bool fresh = of[i].seg != seg;
+        if (fresh) {
+          of[i].key = key;
+          for (int w = 0; w < 4; ++w) of[i].cols[w] = 0u;
+          of[i].seg = seg;
+        }
+        if (of[i].key == key || i == 1) {
+          of[i].key = min(of[i].key, key);
+          of[i].cols[c >> 5] |= m << (c & 31);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+  }
+  if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&s.spoils) = 1u;
+}
+
 // Where run i of `runs` starts in a list of `total`.
 __device__ __forceinline__ long long cut_at(long long total, int i, int runs) {
   if (total < (1 << 20)) return (unsigned)total * (unsigned)i / (unsigned)runs;  // far cheaper
@@ -380,9 +441,10 @@ struct Walk {
     const int x = tile0 + i;
     return (x < s.sink_tiles ? x : s.first + x - s.sink_tiles) * kKeys;
   }
-  // Whether the tile at `base` holds keys that no query of the unit sees.
-  __device__ bool ragged(int base, int pages) const {
-    return pages != 0xFF || base + kKeys - 1 > s.t1 || (base < s.lo && base + kKeys > a.sinks);
+  // Whether some query of the unit does not see some key of the tile at `base`.
+  __device__ bool mixed(int base, int pages) const {
+    return pages != 0xFF || base + kKeys - 1 > s.t0 ||
+           (base <= s.t1 - a.window && base + kKeys > a.sinks);
   }
 };
 
@@ -401,16 +463,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == kLoadWarp * 32) {
     sm.aborted = 0;
+    sm.spoils = 0;
+    for (int i = 0; i < kSpoils; ++i) sm.spoil[i].seg = -1;
     bar_init(&sm.q_full, 1);
     bar_init(&sm.q_free, 1);
-    for (int i = 0; i < kBufs; ++i) bar_init(&sm.full[i], 1), bar_init(&sm.empty[i], 2);
+    for (int i = 0; i < kBufs; ++i) bar_init(&sm.full[i], 1), bar_init(&sm.empty[i], 3);
     for (int x = 0; x < 2; ++x) {
       bar_init(&sm.s_full[x], 1);
       bar_init(&sm.p_full[x], 8);
       bar_init(&sm.o_full[x], 1);
       bar_init(&sm.o_free[x], 8);
     }
-    for (int i = 0; i < kBufs; ++i) bar_init(&sm.v_ready[i], 1);
+    for (int i = 0; i < kBufs; ++i) bar_init(&sm.v_ready[i], 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     prefetch_map(&qmap);
     prefetch_map(&kmap);
@@ -673,24 +737,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kFixWarp) {
-    // ================================================================ fixer
-    int fill = 0, ntile = 0;
+  } else if (warp >= kFixWarp) {
+    // ================================================================ fixers
+    int fill = 0, ntile = 0, seg = -1;
     bool ok = true;
     while (ok && w.next()) {
+      ++seg;
       for (int i = 0; i < w.tiles && ok; ++i, ++ntile) {
         for (int kv = 0; kv < 2; ++kv, ++fill) {
           const int buf = fill % kBufs;
           ok = warp_wait(sm, &sm.full[buf], (fill / kBufs) & 1, a.flags);
           if (!ok) break;
           const int rec = sm.rec[ntile % kRecs], base = (rec >> 8) * kKeys, pages = rec & 0xFF;
-          if (kv == 1 && w.ragged(base, pages)) {
-            for (int r = lane; r < kKeys; r += 32) {
-              const int key = base + r;
+          if (kv == 1 && w.mixed(base, pages)) {
+            // this warp's 64 rows: 8 groups of 8 rows, 2 KB each
+            const int half = warp - kFixWarp;
+            unsigned char* v = ring + buf * kBufBytes + half * (kBufBytes / 2);
+            for (int r = lane; r < 64; r += 32) {
+              const int key = base + half * 64 + r;
               const bool seen = key <= w.s.t1 && (key < a.sinks || key >= w.s.lo) &&
-                                (pages >> (r / kPage) & 1);
+                                (pages >> ((half * 64 + r) / kPage) & 1);
               if (!seen) {
-                unsigned char* p = ring + buf * kBufBytes + (r >> 3) * 2048 + (r & 7) * 128;
+                unsigned char* p = v + (r >> 3) * 2048 + (r & 7) * 128;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                   const int cc = ((c + lane) & 7) * 16;
@@ -699,6 +767,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
+            __syncwarp();
+            uint32_t bad = 0;  // an exponent of all ones carries into the bit above it
+#pragma unroll 8
+            for (int it = 0; it < 32; ++it) {
+              const uint4 x = *reinterpret_cast<const uint4*>(v + it * 512 + lane * 16);
+              bad |= ((x.x & 0x7C007C00u) + 0x04000400u) | ((x.y & 0x7C007C00u) + 0x04000400u) |
+                     ((x.z & 0x7C007C00u) + 0x04000400u) | ((x.w & 0x7C007C00u) + 0x04000400u);
+            }
+            if (__any_sync(0xffffffffu, (bad & 0x80008000u) != 0))
+              spoilt_rows(sm, v, base + half * 64, seg, half);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
           __syncwarp();
@@ -720,8 +798,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* mine = &sm.swap[x][half][row];
     const float* other = &sm.swap[x][half ^ 1][row];
     uint32_t sph = 0, oph = 0;
+    int seg = -1;
     uint32_t ntile = 0;  // key tiles so far, of the CTA
     while (w.next()) {
+      ++seg;
       // one query tile: side x of TMEM has every second key tile of the same rows
       const int xq = w.two ? x : 0, step = w.two ? 1 : 2, first_tile = w.two ? 0 : x;
       const int i = w.i0 + (xq * kTileRows + row) / G;  // the row's query
@@ -851,6 +931,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(o, to + 32 * c);
           wait_ld();
           keep_ld(o);
+          if (*reinterpret_cast<volatile uint32_t*>(&sm.spoils) != 0) {
+            for (int e = 0; e < kSpoils; ++e) {
+              const Spoil& sp = sm.spoil[e];
+              if (sp.seg != seg || sp.key > t || (sp.key >= a.sinks && sp.key <= t - a.window))
+                continue;
+              const uint32_t cols = sp.cols[half * 2 + c];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = cols >> k & 1u ? 0x7FC00000u : o[k];
+            }
+          }
           if (valid && direct) {
             uint32_t h[16];
 #pragma unroll

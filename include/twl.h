@@ -336,7 +336,10 @@ twl_status twl_sparse_decode_noalloc(const void* q, int32_t num_q_heads, const t
  * sinks >= 0, window >= 1; window = INT32_MAX sees every token.  o = softmax(sm_scale q K^T) V
  * over the seen keys (fp16 K/V, fp32 sums), lse = natural-log sum of exp of the scaled scores.
  * Only pages that hold a seen key are read: the table may have -1 for the others.  K and V rows
- * nobody sees may hold anything (NaN included).  sm_scale must be positive and finite.
+ * nobody sees may hold anything (NaN included), and a row that is not finite reaches only the
+ * queries that see it: a K row all of their o, a V row the columns that are not finite (in a chunk
+ * as NaN; where a block of 256 / (Hq / Hkv) queries sees more than two such rows in part, the
+ * columns of the further ones may be NaN for all of its queries that see the first).  sm_scale must be positive and finite.
  *
  * twl_window_decode: one token per sequence, the last one (t = seq_lens[b] - 1; it is in the
  *   cache already, see twl_append_token).

@@ -350,3 +350,185 @@ def test_int4_decode(hq, hkv, sinks, window, vscale):
     assert torch.equal(o, again) and torch.equal(lse, lse2)
     assert all(torch.equal(x, y) for x, y in zip(before, (layer.k, layer.v, n)))
     assert layer.status() == (twl.TWL_OK, 0)
+
+
+# ------------------------------------------------------------------ where such kernels go wrong
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 2), (16, 2)])
+@pytest.mark.parametrize("sinks,window", [(0, ALL), (4, 60), (150, 40)])
+def test_rows_that_are_not_finite_reach_only_their_queries(hq, hkv, sinks, window):
+    from adaptive_top_sparse_b200.layer import DecodeLayer
+    n, qn = 420, 333
+    table, lens, pages = _deal([n], 5)
+    k, v = _rand(1, pages, hkv, PAGE, D), _rand(2, pages, hkv, PAGE, D)
+    q = _rand(3, qn, hq, D)
+    kk, vv = _rows(k, table, 0, n).double(), _rows(v, table, 0, n).double()   # before the planting
+    spoilt_v = {100: (7, math.nan), 300: (100, math.inf), 333: (64, -math.inf)}
+    for key, (col, value) in spoilt_v.items():
+        v[table[0, key // PAGE], 0, key % PAGE, col] = value
+    bad_k = 380
+    k[table[0, bad_k // PAGE], 0, bad_k % PAGE, 3] = math.nan
+    layer = DecodeLayer(k, v, table, lens, hq, hkv)
+    start = torch.tensor([0, qn], dtype=torch.int32, device="cuda")
+    o, lse = layer.window_prefill(q, start, sinks, window)
+    t = torch.arange(n - qn, n, device="cuda")
+    seen = _seen(t, n, sinks, window)
+    want, wlse, big = _attend(q.double(), kk, vv, seen)
+    group = hq // hkv
+    spoilt = torch.zeros_like(o, dtype=torch.bool)
+    for key, (col, _) in spoilt_v.items():
+        spoilt[seen[:, key], :group, col] = True
+    spoilt[seen[:, bad_k], :group] = True
+    assert torch.equal(~o.isfinite(), spoilt)
+    far = (o.double() - want).abs()[~spoilt].max().item()
+    assert far <= 3 * 2.0 ** -11 * 6.0
+    fine = ~seen[:, bad_k, None] | (torch.arange(hq, device="cuda") >= group)
+    assert (lse.double() - wlse)[fine].abs().max().item() <= 2.0 ** -18 * (1 + big)
+    assert not lse[~fine].isfinite().any()
+    # one token: the same for its heads
+    o, lse = layer.window_decode(q[-1:], sinks, window)
+    spoilt = spoilt[-1]
+    assert torch.equal(~o[0].isfinite(), spoilt)
+    assert (o[0].double() - want[-1]).abs()[~spoilt].numel() == 0 or \
+        (o[0].double() - want[-1]).abs()[~spoilt].max().item() <= 2.0 ** -17 * 6.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,hq,hkv", [(4096, 1, 1), (500, 16, 8), (161, 4, 2), (160, 8, 1)])
+def test_many_sequences(batch, hq, hkv):
+    """Batches up to the largest, ragged, some empty: one token, chunks of 0-40, a 4-bit cache."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer, Int4Layer
+    g = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, 70, (batch,), generator=g).tolist()
+    lens[7], lens[8] = 900, 0
+    table, n, pages = _deal(lens, 3, extra_pages=1, spare=0)
+    k, v = _rand(1, pages, hkv, PAGE, D), _rand(2, pages, hkv, PAGE, D)
+    qn = [min(m, int(x)) for m, x in zip(lens, torch.randint(0, 41, (batch,), generator=g))]
+    start = torch.tensor([0] + qn).cumsum(0).int()
+    q, qp = _rand(3, batch, hq, D), _rand(4, int(start[-1]), hq, D)
+    sinks, window = 3, 48
+    layer = DecodeLayer(k, v, table, n, hq, hkv)
+    o, lse = layer.window_decode(q, sinks, window)
+    op, lsep = layer.window_prefill(qp, start.cuda(), sinks, window)
+    four = Int4Layer.from_fp16(k, v, table, n.clone(), hq, hkv)
+    kn, vn = _rand(5, batch, hkv, D), _rand(6, batch, hkv, D)
+    o4, lse4 = four.decode(q, kn, vn, sinks, window)
+    assert four.seq_lens.tolist() == [m + 1 for m in lens]
+    assert layer.status() == (twl.TWL_OK, 0) and four.status() == (twl.TWL_OK, 0)
+    assert bool((o[8] == 0).all()) and bool((lse[8] == -math.inf).all())
+    for b in [0, 1, 7, 8, 9, batch // 2, batch - 1] + list(range(100, batch, batch // 12)):
+        m = lens[b]
+        t = torch.tensor([m - 1], device="cuda")
+        kk, vv = _rows(k, table, b, m).double(), _rows(v, table, b, m).double()
+        if m:
+            want = _attend(q[b:b + 1].double(), kk, vv, _seen(t, m, sinks, window))
+            _check(o[b:b + 1], lse[b:b + 1], want[0], want[1], 6.0, want[2], False)
+        rows = slice(int(start[b]), int(start[b + 1]))
+        if qn[b]:
+            t = torch.arange(m - qn[b], m, device="cuda")
+            want = _attend(qp[rows].double(), kk, vv, _seen(t, m, sinks, window))
+            _check(op[rows], lsep[rows], want[0], want[1], 6.0, want[2], True)
+        m += 1
+        t = torch.tensor([m - 1], device="cuda")
+        kk = _unquantise(_rows(four.k, table, b, m), _rows(four.k_sz, table, b, m))
+        vv = _unquantise(_rows(four.v, table, b, m), _rows(four.v_sz, table, b, m))
+        want = _attend(q[b:b + 1].double(), kk, vv, _seen(t, m, sinks, window))
+        _check(o4[b:b + 1], lse4[b:b + 1], want[0], want[1], 6.0, want[2], False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,lens,qn,sinks,window", [
+    (8, 1, [9000], [4000], 0, ALL),              # one long chunk, keys of many runs
+    (4, 4, [33000, 5], [7, 5], 4, 32000),        # a few queries far behind: every unit is cut
+    (2, 1, [2500, 2500, 0], [2500, 1, 0], 130, 700),
+    (16, 2, [5000] * 9, [1] * 9, 64, 4096)])
+def test_long_chunks(hq, hkv, lens, qn, sinks, window):
+    from adaptive_top_sparse_b200.layer import DecodeLayer
+    table, n, pages = _deal(lens, 11)
+    k, v = _rand(1, pages, hkv, PAGE, D), _rand(2, pages, hkv, PAGE, D)
+    start = torch.tensor([0] + qn).cumsum(0).int()
+    q = _rand(3, int(start[-1]), hq, D, scale=2.0)
+    layer = DecodeLayer(k, v, table, n, hq, hkv)
+    for _ in range(2):
+        o, lse = layer.window_prefill(q, start.cuda(), sinks, window)
+        for b, m in enumerate(lens):
+            kk, vv = _rows(k, table, b, m).double(), _rows(v, table, b, m).double()
+            for r in range(0, qn[b], 500):       # the definition in 64 bits, 500 rows at a time
+                rows = slice(int(start[b]) + r, min(int(start[b]) + r + 500, int(start[b + 1])))
+                t = torch.arange(m - qn[b] + r, m - qn[b] + r + rows.stop - rows.start, device="cuda")
+                want, wlse, big = _attend(q[rows].double(), kk, vv, _seen(t, m, sinks, window))
+                _check(o[rows], lse[rows], want, wlse, 6.0, big, True)
+    assert layer.status() == (twl.TWL_OK, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 1)])
+def test_long_contexts(hq, hkv):
+    """One token behind the longest context a table may hold, fp16 and in 4 bits."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer, Int4Layer
+    lens = [PAGE * 32768 - 1, 39999]
+    table, n, pages = _deal(lens, 2, extra_pages=0, spare=0)
+    table = torch.nn.functional.pad(table, (0, 32768 - table.shape[1]), value=-1)[:, :32768].contiguous()
+    k, v = _rand(1, pages, hkv, PAGE, D), _rand(2, pages, hkv, PAGE, D)
+    q = _rand(3, 2, hq, D, scale=2.0)
+    layer = DecodeLayer(k, v, table, n, hq, hkv)
+    four = Int4Layer.from_fp16(k, v, table, n.clone(), hq, hkv)
+    kn, vn = _rand(4, 2, hkv, D), _rand(5, 2, hkv, D)
+    for sinks, window in ((0, ALL), (5, 300000)):
+        four.seq_lens.copy_(n)
+        o, lse = (x.clone() for x in layer.window_decode(q, sinks, window))
+        o4, lse4 = four.decode(q, kn, vn, sinks, window)
+        for b, m in enumerate(lens):
+            t = torch.tensor([m - 1], device="cuda")
+            want = _attend(q[b:b + 1].double(), _rows(k, table, b, m).double(),
+                           _rows(v, table, b, m).double(), _seen(t, m, sinks, window))
+            _check(o[b:b + 1], lse[b:b + 1], want[0], want[1], 6.0, want[2], False)
+            m, t = m + 1, t + 1
+            kk = _unquantise(_rows(four.k, table, b, m), _rows(four.k_sz, table, b, m))
+            vv = _unquantise(_rows(four.v, table, b, m), _rows(four.v_sz, table, b, m))
+            want = _attend(q[b:b + 1].double(), kk, vv, _seen(t, m, sinks, window))
+            _check(o4[b:b + 1], lse4[b:b + 1], want[0], want[1], 6.0, want[2], False)
+    o4, _ = four.decode(q, kn, vn)               # the first sequence is full now: left alone
+    assert four.seq_lens.tolist() == [PAGE * 32768, 40000]
+    assert bool((o4[0] == 0).all()) and four.status()[0] == twl.TWL_ERR_BAD_INDEX
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Two layers on two streams, all calls in flight together, give what they give alone."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer, Int4Layer
+    sides = []
+    for s in range(2):
+        lens = [300 + 700 * s, 2000, 17]
+        table, n, pages = _deal(lens, s, extra_pages=2, spare=8)
+        k, v = _rand(10 + s, pages, 2, PAGE, D), _rand(20 + s, pages, 2, PAGE, D)
+        layer = DecodeLayer(k, v, table, n, 8, 2)
+        four = Int4Layer.from_fp16(k, v, table, n, 8, 2)
+        start = torch.tensor([0, 200, 500, 517], dtype=torch.int32, device="cuda")
+        q, qp = _rand(30 + s, 3, 8, D), _rand(40 + s, 517, 8, D)
+        parent = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+        out = layer.window_prefill(qp, start)
+        manager = layer.pages()
+        sides.append((layer, four, manager, q, qp, start, parent, out, torch.cuda.Stream()))
+
+    def calls(layer, four, manager, q, qp, start, parent, out, stream):
+        manager.remap(parent, None, 4, 100000, stream=stream)
+        layer.window_decode(q, 4, 500, stream=stream)
+        four.decode(q, sinks=4, window=500, stream=stream)
+        layer.window_prefill(qp, start, 4, 300, out, stream=stream)
+
+    def results(layer, four, manager, q, qp, start, parent, out, stream):
+        return [x.clone() for x in (layer.o, layer.lse, four.o, four.lse, *out, layer.page_table)]
+
+    alone = []
+    for side in sides:
+        calls(*side)
+        torch.cuda.synchronize()
+        alone.append(results(*side))
+    for _ in range(20):
+        for side in sides:
+            calls(*side)
+    torch.cuda.synchronize()
+    for side, want in zip(sides, alone):
+        assert all(torch.equal(x, y) for x, y in zip(results(*side), want))
+        assert side[0].status() == (twl.TWL_OK, 0) and side[2].status() == (twl.TWL_OK, 0)
