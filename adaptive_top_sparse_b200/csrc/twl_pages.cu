@@ -262,29 +262,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
-  // ---- what stays: the entries of 512 logical pages of a slot at a time
+  // ---- what stays: the entries of 512 logical pages of a slot at a time.  What a thread found in
+  // its first stretch, and a warp for its first slot, stays in registers over the barrier (that is
+  // all of it unless the tables are large).
   const int chunks = (a.max_pages + kThreads - 1) / kThreads;
+  int my_page = -1;
+  Slot my_slot = {-1, 0, 0, false, false};
   for (int item = blockIdx.x; item < a.batch * chunks; item += gridDim.x) {
     const int b = item / chunks, j = (item % chunks) * kThreads + tid;
     const Slot s = slot_of(a, keeper, b, &err);
+    int page = -1;
     if (j < a.max_pages) {
       int from;
-      const int page = next_entry(a, s, j, &from, &err);
+      page = next_entry(a, s, j, &from, &err);
       a.next[(size_t)b * a.max_pages + j] = page;
       if (page >= 0) mark(a, page);
     }
+    if (item == (int)blockIdx.x) my_page = page, my_slot = s;
   }
   // ---- what is wanted: a warp per slot, over the pages behind its whole ones
-  for (int b = blockIdx.x + gridDim.x * (tid >> 5); b < a.batch; b += gridDim.x * kWarps) {
+  const int warps = gridDim.x * kWarps, warp = blockIdx.x + gridDim.x * (tid >> 5);
+  int my_n = 0, my_need = 0;
+  unsigned my_want = 0;  // of its first 32 such pages
+  for (int b = warp; b < a.batch; b += warps) {
     const Slot s = slot_of(a, keeper, b, &err);
     int wants = 0, copy = -1;
     for (int j = s.n / kPage + lane; j < s.need; j += 32) {
       int from = -1;
-      if (next_entry(a, s, j, &from, &err) < 0) ++wants;
+      if (next_entry(a, s, j, &from, &err) < 0) {
+        ++wants;
+        if (b == warp && j < s.n / kPage + 32) my_want = 1;
+      }
       if (from >= 0) copy = from;
     }
     wants = __reduce_add_sync(0xffffffffu, wants);
     copy = __reduce_max_sync(0xffffffffu, copy);
+    if (b == warp) my_n = s.n, my_need = s.need;
     if (lane == 0) {
       n_of[b] = s.n;
       need_of[b] = s.need;
@@ -292,17 +305,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       from_of[b] = copy;
     }
   }
+  my_want = __ballot_sync(0xffffffffu, my_want != 0);
   err = __syncthreads_or(err) ? TWL_FLAG_BAD_INDEX : 0u;
   err = grid_barrier(a, err, &sh_word);
 
   if (err == 0) {
+    // the slots' counts are under way while the bitmap is counted
+    int my_wants = tid < a.batch ? __ldcg(wants_of + tid) : 0;
+    int my_from = tid < a.batch ? __ldcg(from_of + tid) : -1;
     count_used(a, prefix, scan_sh);
     int* want_prefix = keeper;
     int wanted = 0, ncopies = 0;
     for (int base = 0; base < a.batch; base += kThreads) {
       const int b = base + tid;
-      const int c = b < a.batch ? __ldcg(wants_of + b) : 0;
-      const int f = b < a.batch && __ldcg(from_of + b) >= 0 ? 1 : 0;
+      if (base > 0) {
+        my_wants = b < a.batch ? __ldcg(wants_of + b) : 0;
+        my_from = b < a.batch ? __ldcg(from_of + b) : -1;
+      }
+      const int c = my_wants, f = my_from >= 0 ? 1 : 0;
       int total;
       int ex = block_exclusive_scan(c, scan_sh, &total);
       if (b < a.batch) want_prefix[b] = wanted + ex;
@@ -320,20 +340,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b = item / chunks, j = (item % chunks) * kThreads + tid;
         if (j < a.max_pages) {
           const size_t i = (size_t)b * a.max_pages + j;
-          const int page = __ldcg(a.next + i);
-          if (page >= 0 || j < __ldcg(n_of + b) / kPage || j >= __ldcg(need_of + b))
-            a.table[i] = page;
+          const bool mine = item == (int)blockIdx.x;
+          const int page = mine ? my_page : __ldcg(a.next + i);
+          const int n = mine ? my_slot.n : __ldcg(n_of + b);
+          const int need = mine ? my_slot.need : __ldcg(need_of + b);
+          if (page >= 0 || j < n / kPage || j >= need) a.table[i] = page;
         }
       }
-      for (int b = blockIdx.x + gridDim.x * (tid >> 5); b < a.batch; b += gridDim.x * kWarps) {
+      for (int b = warp; b < a.batch; b += warps) {
         int rank = want_prefix[b];
-        const int n = __ldcg(n_of + b), need = __ldcg(need_of + b);
+        const bool mine = b == warp;
+        const int n = mine ? my_n : __ldcg(n_of + b), need = mine ? my_need : __ldcg(need_of + b);
         for (int base = n / kPage; base < need; base += 32) {
           const int j = base + lane;
           const size_t i = (size_t)b * a.max_pages + j;
-          const bool want = j < need && __ldcg(a.next + i) < 0;
-          const unsigned all = __ballot_sync(0xffffffffu, want);
-          if (want)
+          const unsigned all =
+              mine && base == n / kPage
+                  ? my_want
+                  : __ballot_sync(0xffffffffu, j < need && __ldcg(a.next + i) < 0);
+          if (all >> lane & 1u)
             a.table[i] = page_of_rank<false>(a, prefix, rank + __popc(all & ((1u << lane) - 1u)));
           rank += __popc(all);
         }

@@ -59,7 +59,7 @@ struct Smem {
   // barriers
   uint64_t q_full, q_free;
   uint64_t full[kBufs], empty[kBufs];
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
   uint64_t v_ready[kBufs];  // V of the buffer is loaded and its unseen rows are zero
   uint32_t tmem;
   int aborted;
@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kBufs; ++i) bar_init(&sm.full[i], 1), bar_init(&sm.empty[i], 3);
     for (int x = 0; x < 2; ++x) {
       bar_init(&sm.s_full[x], 1);
+      bar_init(&sm.p_half[x], 8);
       bar_init(&sm.p_full[x], 8);
       bar_init(&sm.o_full[x], 1);
       bar_init(&sm.o_free[x], 8);
@@ -657,16 +658,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&sm.o_free[x], free_ph >> x & 1);
           free_ph ^= 1u << x;
         }
-        wait(&sm.p_full[x], p_ph >> x & 1);
+        const uint64_t v0 = dv + (uint64_t)(vb * (kBufBytes >> 4));
+        const uint32_t ph = p_ph >> x & 1;
         p_ph ^= 1u << x;
+        // half of the weights come first: columns 0 .. 31 and 64 .. 95 (those of columns 64 .. lie
+        // over those columns' scores)
+        wait(&sm.p_half[x], ph);
         if (!ok) return;
         fence_after();
-        const uint64_t v0 = dv + (uint64_t)(vb * (kBufBytes >> 4));
-        // the weights of columns 64 .. lie over those columns' scores
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + 256 + x * 128, tmem + x * 128 + (k >> 2) * 64 + (k & 3) * 8,
-                 v0 + k * (4096 >> 4), !first || k > 0);
+        for (int k = 0; k < 8; ++k) {
+          const int ks = (k & 1) + (k >> 1 & 1) * 4 + (k >> 2) * 2;  // 0 1 4 5, 2 3 6 7
+          if (k == 4) {
+            wait(&sm.p_full[x], ph);
+            if (!ok) return;
+            fence_after();
+          }
+          mma_ts(tmem + 256 + x * 128, tmem + x * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
+                 v0 + ks * (4096 >> 4), !first || k > 0);
+        }
       };
       while (ok && w.next()) {
         wait(&sm.q_full, q_ph);
@@ -903,6 +913,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // the weights' columns lie over scores of this thread that have been read by now
           tmem_st16(ts + (c >> 1), p);
+          if (c == 0) {
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm.p_half[x]);
+          }
         }
         l += __uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32));
         wait_st();
