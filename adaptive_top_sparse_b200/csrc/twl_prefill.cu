@@ -43,6 +43,9 @@ constexpr int kRows = 256, kTileRows = 128, kKeys = 128;
 constexpr int kThreads = 640;
 constexpr int kBufBytes = 32768, kBufs = 5;
 constexpr int kQBytes = 65536;
+// What a unit costs beside its key tiles (filling and emptying the pipeline, masks, the output), in
+// tiles: places in the flat list that hold no work, so that a run of many short units is shorter.
+constexpr int kUnitCost = 2;
 constexpr int kRecs = 8;
 constexpr int kSpoils = 16, kSpoilsPer = 4;  // of the CTA's last segments; of one (two a fixer)
 constexpr int kMmaWarp = 16, kLoadWarp = 17, kFixWarp = 18;
@@ -405,11 +408,12 @@ struct Walk {
   static constexpr int kQueries = kRows / G;
   const Args& a;
   long long at, end;     // place in the flat list
-  int b, kvh, qt, tile;  // of the next segment
+  int b, kvh, qt, tile;  // of the next segment (tile: its place in the unit)
   Chunk c;
   // the current segment
   Span s;
   int i0, tile0, tiles;  // first query, first key tile, key tiles
+  long long start;       // the unit's place in the list
   bool whole, two;       // the whole unit; it has rows in the second query tile
 
   __device__ Walk(const Args& a, const Smem& sm, long long f0, long long f1)
@@ -417,23 +421,27 @@ struct Walk {
     if (at < end) c = chunk_of(a, b, false);
   }
   __device__ bool next() {
-    if (at >= end) return false;
-    while (qt * kQueries >= c.qn) {
-      qt = 0;
-      if (++kvh >= a.hkv || c.qn == 0) {
-        kvh = 0;
-        c = chunk_of(a, ++b, false);
+    do {
+      if (at >= end) return false;
+      while (qt * kQueries >= c.qn) {
+        qt = 0;
+        if (++kvh >= a.hkv || c.qn == 0) {
+          kvh = 0;
+          c = chunk_of(a, ++b, false);
+        }
       }
-    }
-    i0 = qt * kQueries;
-    s = span_of(a, c, i0, kQueries);
-    tile0 = tile;
-    tiles = (int)min((long long)(s.tiles - tile), end - at);
+      i0 = qt * kQueries;
+      s = span_of(a, c, i0, kQueries);
+      tile0 = tile;
+      start = at - tile;
+      const int take = (int)min((long long)(s.tiles + kUnitCost - tile), end - at);
+      tiles = min(tile + take, s.tiles) - tile;
+      at += take;
+      tile += take;
+      if (tile == s.tiles + kUnitCost) tile = 0, ++qt;
+    } while (tiles <= 0);
     whole = tiles == s.tiles;
     two = i0 + kTileRows / G < c.qn;
-    at += tiles;
-    tile += tiles;
-    if (tile == s.tiles) tile = 0, ++qt;
     return true;
   }
   // First token of the segment's key tile i.
@@ -491,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Chunk c = chunk_of(a, b, blockIdx.x == 0 && lane == 0);
     long long sum = 0;
     for (int i = lane * kQueries; i < c.qn; i += 32 * kQueries)
-      sum += span_of(a, c, i, kQueries).tiles;
+      sum += span_of(a, c, i, kQueries).tiles + kUnitCost;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) prefix[b + 1] = sum;
@@ -535,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Chunk c = chunk_of(a, x, false);
     for (int q0 = 0;; q0 += 32) {  // the unit that holds tile `rest` of this kv-head
       const int i = (q0 + lane) * kQueries;
-      const int t = i < c.qn ? span_of(a, c, i, kQueries).tiles : 0;
+      const int t = i < c.qn ? span_of(a, c, i, kQueries).tiles + kUnitCost : 0;
       int sum = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -989,8 +997,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         part[kRows * (kHeadDim + 1) + prow] = active ? l : 0.f;
       }
       // ---- a cut unit: the run that arrives last merges the partials, in run order
-      const long long fs = w.at - w.tiles - w.tile0;  // the unit's first tile in the list
-      const int first = run_of(fs, total, runs), last = run_of(fs + w.s.tiles - 1, total, runs);
+      const int first = run_of(w.start, total, runs),
+                last = run_of(w.start + w.s.tiles - 1, total, runs);
       __threadfence();
       named_sync(1, 512);
       if (tid == 0)
