@@ -882,8 +882,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the halves agree on the row's maximum (they write again only behind the next scores,
         // which need both of them)
         *mine = m0;
+        uint32_t v[32];
+        tmem_ld32(v, ts);  // the first columns again, under way while the halves meet
         named_sync(pair_bar, 64);
-        if (!live) continue;
+        if (!live) {
+          wait_ld();
+          continue;
+        }
         const float top = fmaxf(m0, *other) * a.scale_log2;
         if (__any_sync(0xffffffffu, top > m + kSlack)) {
           const float mn = fmaxf(m, top);
@@ -909,16 +914,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < 64; c += 32) {
           uint32_t p[16];
+          wait_ld();
+          keep_ld(v);
           if (dark >> (c / 32) & 1) {
 #pragma unroll
             for (int k = 0; k < 16; ++k) p[k] = 0u;
           } else {
-            uint32_t v[32];
-            tmem_ld32(v, ts + c);
-            wait_ld();
-            keep_ld(v);
             weights(v, scale2, shift2, sum, p);
           }
+          if (c == 0) tmem_ld32(v, ts + 32);
           // the weights' columns lie over scores of this thread that have been read by now
           tmem_st16(ts + (c >> 1), p);
           if (c == 0) {
