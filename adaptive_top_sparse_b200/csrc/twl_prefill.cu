@@ -406,7 +406,7 @@ __device__ __forceinline__ int run_of(long long f, long long total, int runs) {
 template <int G>
 struct Walk {
   static constexpr int kQueries = kRows / G;
-  const Args& a;
+  const Args* args;
   long long at, end;     // place in the flat list
   int b, kvh, qt, tile;  // of the next segment (tile: its place in the unit)
   Chunk c;
@@ -417,10 +417,11 @@ struct Walk {
   bool whole, two;       // the whole unit; it has rows in the second query tile
 
   __device__ Walk(const Args& a, const Smem& sm, long long f0, long long f1)
-      : a(a), at(f0), end(f1), b(sm.b), kvh(sm.kvh), qt(sm.qt), tile(sm.tile) {
+      : args(&a), at(f0), end(f1), b(sm.b), kvh(sm.kvh), qt(sm.qt), tile(sm.tile) {
     if (at < end) c = chunk_of(a, b, false);
   }
   __device__ bool next() {
+    const Args& a = *args;
     do {
       if (at >= end) return false;
       while (qt * kQueries >= c.qn) {
@@ -452,7 +453,7 @@ struct Walk {
   // Whether some query of the unit does not see some key of the tile at `base`.
   __device__ bool mixed(int base, int pages) const {
     return pages != 0xFF || base + kKeys - 1 > s.t0 ||
-           (base <= s.t1 - a.window && base + kKeys > a.sinks);
+           (base <= s.t1 - args->window && base + kKeys > args->sinks);
   }
 };
 
@@ -686,13 +687,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                  v0 + ks * (4096 >> 4), !first || k > 0);
         }
       };
-      while (ok && w.next()) {
+      auto first_scores = [&](int b) {  // of a unit, for side 0
         wait(&sm.q_full, q_ph);
         q_ph ^= 1;
-        wait_k(kb);
-        if (!ok) break;
+        wait_k(b);
+        if (!ok) return;
         fence_after();
-        scores(0, kb, false);
+        scores(0, b, false);
+      };
+      Walk<G> ahead = w;
+      bool more = w.next(), begun = false;
+      while (ok && more) {
+        if (!begun) first_scores(kb);
+        if (!ok) break;
+        begun = false;
+        ahead = w;
+        more = ahead.next();
         if (w.two) {
           // two query tiles, every key tile for both
           scores(1, kb, true);
@@ -709,6 +719,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (i == 1) {
                 mma_commit(&sm.o_full[x]);
                 ++units[x];
+                if (x == 0 && more && ahead.two) {
+                  // the next unit's first scores, while side 1 of this one finishes
+                  first_scores(kn);
+                  begun = true;
+                  if (!ok) break;
+                }
               } else {
                 if (x == 0) wait_k(kn);
                 else wait_v(next_buf(kn));
@@ -752,6 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             kb = kn;
           }
         }
+        w = ahead;
       }
     }
     __syncwarp();

@@ -339,7 +339,8 @@ twl_status twl_sparse_decode_noalloc(const void* q, int32_t num_q_heads, const t
  * nobody sees may hold anything (NaN included), and a row that is not finite reaches only the
  * queries that see it: a K row all of their o, a V row the columns that are not finite (in a chunk
  * as NaN; where a block of 256 / (Hq / Hkv) queries sees more than two such rows in part, the
- * columns of the further ones may be NaN for all of its queries that see the first).  sm_scale must be positive and finite.
+ * columns of the further ones may be NaN for all of its queries that see the first).  sm_scale must
+ * be positive and finite.
  *
  * twl_window_decode: one token per sequence, the last one (t = seq_lens[b] - 1; it is in the
  *   cache already, see twl_append_token).
@@ -358,7 +359,8 @@ twl_status twl_sparse_decode_noalloc(const void* q, int32_t num_q_heads, const t
  *   fine.  A sequence whose chunk is not inside [0, total_q] or longer than its length, or whose
  *   length is > 16 * max_pages, is skipped (its outputs are not written), and a page that is out
  *   of range is skipped, both with TWL_FLAG_BAD_INDEX.  total_q = 0 launches nothing.
- *   Workspace TWL_OP_WINDOW_PREFILL (batch, num_q_heads, num_kv_heads), zeroed once. */
+ *   Workspace TWL_OP_WINDOW_PREFILL (batch, num_q_heads, num_kv_heads), zeroed once.
+ *   batch * num_kv_heads > 4096 or num_phys_pages * num_kv_heads >= 2^27: TWL_ERR_UNSUPPORTED. */
 twl_status twl_window_decode(const void* q, int32_t num_q_heads, const twl_paged_kv* kv,
                              int32_t sinks, int32_t window, float sm_scale, float* o, float* lse,
                              void* ws, size_t ws_bytes, twl_stream_t stream);
