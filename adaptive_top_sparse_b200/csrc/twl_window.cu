@@ -10,16 +10,20 @@
 // Bound: memory.  A token of one kv-head is 512 B (fp16) or 136 B (4-bit) and every byte is read
 // once; the heads of a GQA group share the read.
 //
-// Work split: a page of 16 tokens of one (sequence, kv-head) group is a tile; the visible tiles of
-// all groups form one flat list that is cut into equal runs, one per CTA, whatever the lengths.  A
-// group that lies inside one run is finished there; a group cut by runs leaves one partial (max,
-// sum, o) per CTA, and the CTA that arrives last merges them in CTA order (so the result does not
-// depend on who is last).  Lengths stay on the device: each CTA derives the list from seq_lens.
+// Work split: a page of 16 tokens (4-bit: two) of one (sequence, kv-head) group is a tile; the
+// visible tiles of all groups form one flat list that is cut into runs, one per CTA, whatever the
+// lengths.  A group that lies inside one run is finished there; a group cut by runs leaves one
+// partial (max, sum, o) per CTA, and the CTA that arrives last merges them in CTA order (so the
+// result does not depend on who is last).  Lengths stay on the device: each CTA derives the list
+// from seq_lens.
 //
 // Inside a CTA the warps take the tiles in turn, each through its own ring of cp.async stages (no
 // barrier in the loop), with transposed products so that the <= 8 heads of a group are the N = 8
 // of mma.m16n8k16:  S^T = K Q^T (16 tokens x 8 heads), O^T = V^T P^T (16 dims x 8 heads); P^T
 // comes from S^T by an 8x8 transpose in registers (movmatrix).
+// Measured (one B200): 16 sequences of 8K-32K tokens, fp16, 204 us (6.2 TB/s, the copy rate is
+// 6.55); 64 x 8K tokens of a 4-bit cache 181 us (3.2 TB/s: 398 instructions a page, half of them
+// the codes' extraction, bound it; 12 warps with two pages a step against 16 with one: 181, 185 us).
 // Precision: o and lse are fp32 results, so P enters as hi + lo fp16 parts (22 bits).  With G <= 4
 // the parts use the two halves of the N = 8 columns and cost nothing; G = 8 takes two products.
 #include "twl_common.cuh"
@@ -357,37 +361,37 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
       if (lf < f1) {
 #pragma unroll
         for (int h = 0; h < kPages; ++h) {
-        const bool ok = (unsigned)lphys[h] < (unsigned)a.num_phys;
-        if (lane == 0) {
-          tile_base[warp][ls][h] = ok ? lpage[h] * kPage : -1;
-          if (!ok && lpage[h] >= 0) raise_flag(a.flags, TWL_FLAG_BAD_INDEX);
-        }
-        const uint32_t st = ring_at + ls * kTile + h * (kTile / kPages);
-        const uint32_t row0 = ok ? (uint32_t)(lphys[h] * a.hkv + lkvh) * kPage : 0u;
-        if constexpr (INT4) {
-          const uint8_t* ks = k_lane + (uint64_t)row0 * 64;
-          const uint8_t* vs = v_lane + (uint64_t)row0 * 64;
-          if (ok) {  // the codes of a page that is not there are not read
-            copy16<0>(st + k_to, ks);
-            copy16<512>(st + k_to, ks);
-            copy16<0>(st + v_to, vs);
-            copy16<512>(st + v_to, vs);  // rows r and r + 8 lie 512 bytes apart
-            if (lane < 8) copy16<0>(st + 2048 + lane * 16, sz_lane + row0);
+          const bool ok = (unsigned)lphys[h] < (unsigned)a.num_phys;
+          if (lane == 0) {
+            tile_base[warp][ls][h] = ok ? lpage[h] * kPage : -1;
+            if (!ok && lpage[h] >= 0) raise_flag(a.flags, TWL_FLAG_BAD_INDEX);
           }
-        } else {
-          const uint8_t* ks = k_lane + (uint64_t)row0 * 256;
-          const uint8_t* vs = v_lane + (uint64_t)row0 * 256;
-          const int c = lane & 15;
-#pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int r = it * 2 + (lane >> 4), tok = lpage[h] * kPage + r;
-            // rows nobody sees are zeroed: a weight of 0 times a stale infinity would be NaN
-            const bool hide = !(ok && tok < ln && (tok < a.sinks || tok >= llo));
-            const uint32_t to = st + r * 256 + ((c ^ (r & 7)) * 16);
-            copy16_or_zero(to, ks + it * 512, hide);
-            copy16_or_zero(to + 4096, vs + it * 512, hide);
+          const uint32_t st = ring_at + ls * kTile + h * (kTile / kPages);
+          const uint32_t row0 = ok ? (uint32_t)(lphys[h] * a.hkv + lkvh) * kPage : 0u;
+          if constexpr (INT4) {
+            const uint8_t* ks = k_lane + (uint64_t)row0 * 64;
+            const uint8_t* vs = v_lane + (uint64_t)row0 * 64;
+            if (ok) {  // the codes of a page that is not there are not read
+              copy16<0>(st + k_to, ks);
+              copy16<512>(st + k_to, ks);
+              copy16<0>(st + v_to, vs);
+              copy16<512>(st + v_to, vs);  // rows r and r + 8 lie 512 bytes apart
+              if (lane < 8) copy16<0>(st + 2048 + lane * 16, sz_lane + row0);
+            }
+          } else {
+            const uint8_t* ks = k_lane + (uint64_t)row0 * 256;
+            const uint8_t* vs = v_lane + (uint64_t)row0 * 256;
+            const int c = lane & 15;
+  #pragma unroll
+            for (int it = 0; it < 8; ++it) {
+              const int r = it * 2 + (lane >> 4), tok = lpage[h] * kPage + r;
+              // rows nobody sees are zeroed: a weight of 0 times a stale infinity would be NaN
+              const bool hide = !(ok && tok < ln && (tok < a.sinks || tok >= llo));
+              const uint32_t to = st + r * 256 + ((c ^ (r & 7)) * 16);
+              copy16_or_zero(to, ks + it * 512, hide);
+              copy16_or_zero(to + 4096, vs + it * 512, hide);
+            }
           }
-        }
         }
         lf += kWarps;
         fetch();
@@ -602,7 +606,8 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int r = 2 * lt + (i & 1) + (i >> 1) * 8;
-              v[i] = *reinterpret_cast<const uint2*>(page + 1024 + v_slot(r, c) * 16 + (lg & 1) * 8);
+              v[i] = *reinterpret_cast<const uint2*>(page + 1024 + v_slot(r, c) * 16 +
+                                                     (lg & 1) * 8);
             }
             const uint32_t x4[4] = {__byte_perm(v[0].x, v[1].x, 0x5410),
                                     __byte_perm(v[0].x, v[1].x, 0x7632),
@@ -633,8 +638,8 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
               const int r = (lane >> 4) * 8 + (lane & 7);
               uint32_t av[4];
               ldmatrix4_trans(av, vb + r * 256 + (((2 * i + ((lane >> 3) & 1)) ^ (r & 7)) * 16));
-              // The tensor core truncates its sums: over the tiles of a long sequence that is a bias
-              // (measured at 32K tokens: 2.3e-6 of |o| instead of 7e-7), so it only sums a tile.
+              // The tensor core truncates its sums: over the tiles of a long sequence that is a
+              // bias (measured at 32K tokens: 2.3e-6 of |o| instead of 7e-7): it only sums a tile.
               float d[4] = {0.f, 0.f, 0.f, 0.f};
               mma_16816(d, av, ph[0], ph[1]);
               if constexpr (G == 8) mma_16816(d, av, pl[0], pl[1]);
@@ -786,7 +791,8 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
           for (int c = lane; c < parts; c += 32) m = fmaxf(m, wt[c * G + h]);
           m = warp_max(m);
           float l = 0.f;
-          for (int c = lane; c < parts; c += 32) l = fmaf(exp2_fast(wt[c * G + h] - m), ls[c * G + h], l);
+          for (int c = lane; c < parts; c += 32)
+            l = fmaf(exp2_fast(wt[c * G + h] - m), ls[c * G + h], l);
           l = warp_sum(l);
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4

@@ -435,8 +435,8 @@ twl_status twl_int4_decode(const void* q, int32_t num_q_heads, const twl_int4_kv
  *   >= num_phys_pages raises TWL_FLAG_BAD_INDEX and nothing is changed.
  * Both: page_table int32 [batch][max_pages], seq_lens int32 [batch], 1 <= num_pools <=
  *   TWL_MAX_POOLS, workspace TWL_OP_PAGES (batch, max_pages, rows = num_phys_pages), zeroed once;
- *   batch > 4096 or num_phys_pages > 8388608 (2^23): TWL_ERR_UNSUPPORTED.  One cooperative launch each
- *   (every SM takes one CTA); a wait that gives up raises TWL_FLAG_TIMEOUT (state undefined). */
+ *   batch > 4096 or num_phys_pages > 8388608 (2^23): TWL_ERR_UNSUPPORTED.  One cooperative launch
+ *   each (every SM takes one CTA); a wait that gives up raises TWL_FLAG_TIMEOUT (state undefined). */
 #define TWL_MAX_POOLS 128
 typedef struct twl_page_pool {
   void* data;

@@ -532,3 +532,95 @@ def test_two_streams_at_once():
     for side, want in zip(sides, alone):
         assert all(torch.equal(x, y) for x, y in zip(results(*side), want))
         assert side[0].status() == (twl.TWL_OK, 0) and side[2].status() == (twl.TWL_OK, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("four_bit", [False, True])
+def test_pools_beyond_32_bit_offsets(four_bit):
+    """Pools of more than 2^32 bytes whose used pages lie at the far end: attention there, then a
+    compaction that moves them to the front, then the same attention bit for bit."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer, Int4Layer, PageManager
+    hq, hkv, lens = 16, 8, [700, 33]
+    pages = 530000 if four_bit else 140000
+    need = [-(-(m + 2) // PAGE) for m in lens]
+    table = torch.full((2, max(need)), -1, dtype=torch.int32, device="cuda")
+    far = pages - 1 - 7 * torch.arange(sum(need), dtype=torch.int32, device="cuda")
+    table[0, :need[0]], table[1, :need[1]] = far[:need[0]], far[need[0]:]
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = _rand(1, 2, hq, D)
+    if four_bit:
+        k, v = (torch.zeros((pages, hkv, PAGE, 64), dtype=torch.uint8, device="cuda") for _ in "kv")
+        ks, vs = (torch.zeros((pages, hkv, PAGE, 2), dtype=torch.float16, device="cuda") for _ in "kv")
+        for i, (c, sz) in enumerate(((k, ks), (v, vs))):
+            g = torch.Generator(device="cuda").manual_seed(i)
+            c[far.long()] = torch.randint(0, 256, (len(far), hkv, PAGE, 64), generator=g,
+                                          device="cuda").to(torch.uint8)
+            sz[far.long()] = _rand(5 + i, len(far), hkv, PAGE, 2, scale=0.3).abs()
+        layer = Int4Layer(k, ks, v, vs, table, n, hq, hkv)
+        kn, vn = _rand(2, 2, hkv, D), _rand(3, 2, hkv, D)
+        o, lse = (x.clone() for x in layer.decode(q, kn, vn))
+        for b in range(2):
+            m = lens[b] + 1
+            kk = _unquantise(_rows(k, table, b, m), _rows(ks, table, b, m))
+            vv = _unquantise(_rows(v, table, b, m), _rows(vs, table, b, m))
+            want = _attend(q[b:b + 1].double(), kk, vv,
+                           torch.ones((1, m), dtype=torch.bool, device="cuda"))
+            _check(o[b:b + 1], lse[b:b + 1], want[0], want[1], vv.abs().max().item(), want[2], False)
+        again = lambda: layer.decode(q)
+    else:
+        k, v = (torch.empty((pages, hkv, PAGE, D), dtype=torch.float16, device="cuda") for _ in "kv")
+        for i, x in enumerate((k, v)):
+            x[far.long()] = _rand(7 + i, len(far), hkv, PAGE, D)
+        layer = DecodeLayer.__new__(DecodeLayer)        # without the derived K data: two pools only
+        layer.k, layer.v, layer.num_q_heads, layer.num_kv_heads, layer.batch = k, v, hq, hkv, 2
+        layer.kv = twl.PagedKV(k, v, table, n, hkv, pages)
+        layer.o = torch.zeros((2, hq, D), device="cuda")
+        layer.lse = torch.zeros((2, hq), device="cuda")
+        layer.ws_window = twl.alloc_workspace(twl.TWL_OP_WINDOW_DECODE, "cuda", batch=2,
+                                              num_q_heads=hq, num_kv_heads=hkv)
+        layer.ws_prefill = None
+        start = torch.tensor([0, 300, 310], dtype=torch.int32, device="cuda")
+        qp = _rand(4, 310, hq, D)
+        o, lse = (x.clone() for x in layer.window_decode(q))
+        op, lsep = layer.window_prefill(qp, start)
+        for b in range(2):
+            m = lens[b]
+            kk, vv = _rows(k, table, b, m).double(), _rows(v, table, b, m).double()
+            t = torch.tensor([m - 1], device="cuda")
+            want = _attend(q[b:b + 1].double(), kk, vv, _seen(t, m, 0, ALL))
+            _check(o[b:b + 1], lse[b:b + 1], want[0], want[1], 6.0, want[2], False)
+            rows = slice(int(start[b]), int(start[b + 1]))
+            t = torch.arange(m - (rows.stop - rows.start), m, device="cuda")
+            want = _attend(qp[rows].double(), kk, vv, _seen(t, m, 0, ALL))
+            _check(op[rows], lsep[rows], want[0], want[1], 6.0, want[2], True)
+        again = lambda: layer.window_decode(q)
+    pools = [layer.k, layer.k_sz, layer.v, layer.v_sz] if four_bit else [k, v]
+    manager = PageManager(pools, table, n)
+    parent = torch.tensor([0, 0], dtype=torch.int32, device="cuda")      # a fork of a far page
+    manager.remap(parent)
+    assert int(manager.compact()) == need[0] + (1 if int(n[0]) % PAGE else 0) and \
+        manager.status() == (twl.TWL_OK, 0)
+    o2, lse2 = again()
+    # the fork's second slot attends with its own query; the first is unchanged
+    assert torch.equal(o2[0], o[0]) and torch.equal(lse2[0], lse[0])
+
+
+@pytest.mark.gpu
+def test_empty_and_allocating_calls():
+    from adaptive_top_sparse_b200.layer import DecodeLayer
+    table, n, pages = _deal([20, 5], 1)
+    k, v = _rand(1, pages, 2, PAGE, D), _rand(2, pages, 2, PAGE, D)
+    layer = DecodeLayer(k, v, table, n, 4, 2)
+    start = torch.zeros(3, dtype=torch.int32, device="cuda")
+    o, lse = layer.window_prefill(_rand(3, 0, 4, D), start)        # no rows at all
+    assert o.shape == (0, 4, D) and lse.shape == (0, 4)
+    q = _rand(4, 6, 4, D)
+    o, lse = layer.window_prefill(q, start)                        # rows, but every chunk empty
+    start = torch.tensor([2, 4, 5], dtype=torch.int32, device="cuda")
+    o, lse = layer.window_prefill(q, start)
+    same = layer.window_prefill(q, start, out=(torch.empty_like(o), torch.empty_like(lse)))
+    assert torch.equal(o[2:5], same[0][2:5]) and torch.equal(lse[2:5], same[1][2:5])
+    for bad in ([0, 7, 7], [3, 2, 6], [-1, 2, 3], [0, 0, 6]):      # outside q, backwards, too long
+        layer.window_prefill(q, torch.tensor(bad, dtype=torch.int32, device="cuda"))
+        assert layer.status(clear=True) == (twl.TWL_ERR_BAD_INDEX, twl.TWL_FLAG_BAD_INDEX)
+    assert layer.status() == (twl.TWL_OK, 0)
