@@ -910,8 +910,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_st();
         }
         m0 = fmaxf(m0, m1);
-        // the halves agree on the row's maximum (they write again only behind the next scores,
-        // which need both of them)
+        // the halves agree on the row's maximum (they write the next one only behind the next
+        // scores, which need both of them)
         *mine = m0;
         uint32_t v[32];
         tmem_ld32(v, ts);  // the first columns again, under way while the halves meet
@@ -971,6 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ntile += w.tiles;
       // ---- the unit's rows
+      named_sync(pair_bar, 64);  // the other half has read the last maximum
       *mine = l;
       named_sync(pair_bar, 64);
       l += *other;
