@@ -247,7 +247,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // 2^x without the special function unit, whose one result in 8 cycles a warp is as much of a bound
 // as the tensor core: x = i + f with f in [-0.5, 0.5] by rounding through 1.5 2^23, 2^f by a
 // polynomial (degree 4, fitted for the least relative error, 2.7e-6), i added to the exponent.
-// Below 2^-125 the result stays there: 0 as fp16.
+// Below 2^-125 the result stays there: 0 as fp16.  NaN does too: such a score reaches the row by
+// its maximum (max3).
 __device__ __forceinline__ float exp2_poly(float x) {
   x = fmaxf(x, -125.f);
   const float i = __fadd_rn(x, 0x1.8p23f);
@@ -258,9 +259,15 @@ __device__ __forceinline__ float exp2_poly(float x) {
   y = fmaf(y, f, 0.9999992847442627f);
   return __uint_as_float(__float_as_uint(y) + (__float_as_uint(i) << 23));
 }
+// Maxima that are NaN when an operand is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float max2(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
 // Two fp32 values in one register pair.
@@ -909,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           wait_st();
         }
-        m0 = fmaxf(m0, m1);
+        m0 = max2(m0, m1);
         // the halves agree on the row's maximum (they write the next one only behind the next
         // scores, which need both of them)
         *mine = m0;
@@ -920,9 +927,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_ld();
           continue;
         }
-        const float top = fmaxf(m0, *other) * a.scale_log2;
-        if (__any_sync(0xffffffffu, top > m + kSlack)) {
-          const float mn = fmaxf(m, top);
+        const float top = max2(m0, *other) * a.scale_log2;
+        if (__any_sync(0xffffffffu, !(top <= m + kSlack))) {
+          // a row that has seen a score of NaN or +inf is NaN from here on: sum, lse and all of o
+          float mn = max2(m, top);
+          if (mn == INFINITY) mn = NAN;
           const float f = exp2_fast(m - ref_of(mn));
           m = mn;
           l *= f;

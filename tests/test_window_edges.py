@@ -33,3 +33,50 @@ def test_chunks_repeat_bit_for_bit(hq, hkv, sinks, window):
                                   _rows(v, table, b, m).double(), _seen(t, m, sinks, window))
         _check(first[0][rows], first[1][rows], want, wlse, 6.0, big, True)
     assert layer.status() == (0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("where", [160, 300, 520])    # a tile all see, one at the edge, the last one
+@pytest.mark.parametrize("qn", [150, 5])              # two query tiles, one
+@pytest.mark.parametrize("copies", [1, 50])           # units cut by runs, and whole ones
+def test_a_score_that_is_not_finite_counts_at_every_key(bad, where, qn, copies):
+    """A K row with a NaN, or with an infinity that makes a score of +inf, at eight keys in a row: no
+    query that sees it gets a finite o or lse, the others are exact.  A score of -inf has weight 0."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer
+    n, hq, hkv, sinks, window = 600, 4, 2, 0, 300
+    table, lens, pages = _deal([n], 5)
+    k, v = _rand(1, pages, hkv, PAGE, D), _rand(2, pages, hkv, PAGE, D)
+    q = _rand(3, qn, hq, D)
+    q[..., 3] = -1.0 if bad == "-inf" else 1.0
+    start = torch.arange(copies + 1, dtype=torch.int32, device="cuda") * qn
+    t = torch.arange(n - qn, n, device="cuda")
+    seen = _seen(t, n, sinks, window)
+    group = torch.arange(hq, device="cuda") < hq // hkv
+    for key in range(where, where + 8):
+        kk = k.clone()
+        kk[table[0, key // PAGE], 0, key % PAGE, 3] = math.nan if bad == "nan" else math.inf
+        # sequences that share all their pages
+        layer = DecodeLayer(kk, v, table.repeat(copies, 1), lens.repeat(copies), hq, hkv)
+        os, lses = layer.window_prefill(q.repeat(copies, 1, 1), start, sinks, window)
+        one, lse1 = layer.window_decode(q[-1:].repeat(copies, 1, 1), sinks, window)
+        # what rows see without the planted one, and heads of the other kv-head with it
+        keep = seen.clone()
+        keep[:, key] = False
+        rows = _rows(k, table, 0, n).double(), _rows(v, table, 0, n).double()
+        without = _attend(q.double(), *rows, keep)
+        whole = _attend(q.double(), *rows, seen)
+        hit = seen[:, key, None] & group
+        want = torch.where(hit[..., None], without[0], whole[0])
+        wlse = torch.where(hit, without[1], whole[1])
+        for c in range(copies):
+            o, lse = os[c * qn:(c + 1) * qn], lses[c * qn:(c + 1) * qn]
+            if bad != "-inf":
+                assert not o[hit].isfinite().any() and not lse[hit].isfinite().any()
+                assert not one[c][hit[-1]].isfinite().any()
+                assert not lse1[c][hit[-1]].isfinite().any()
+            near = torch.zeros_like(hit) if bad == "-inf" else hit
+            _check(o[~near], lse[~near], want[~near], wlse[~near], 6.0, whole[2], True)
+            _check(one[c][~near[-1]], lse1[c][~near[-1]], want[-1][~near[-1]], wlse[-1][~near[-1]],
+                   6.0, whole[2], False)
+        assert layer.status() == (0, 0)
