@@ -239,10 +239,11 @@ class Int4Layer:
         self.device = dev
         self.kv = twl.Int4KV(k, k_sz, v, v_sz, page_table, seq_lens, num_kv_heads, p_phys)
         self.batch = self.kv.batch
-        self.ws = twl.alloc_workspace(twl.TWL_OP_INT4_DECODE, dev, batch=self.batch,
-                                      num_q_heads=num_q_heads, num_kv_heads=num_kv_heads)
         self.o = torch.zeros((self.batch, num_q_heads, 128), dtype=torch.float32, device=dev)
         self.lse = torch.zeros((self.batch, num_q_heads), dtype=torch.float32, device=dev)
+        # behind the other buffers: they too are filled once it is there
+        self.ws = twl.alloc_workspace(twl.TWL_OP_INT4_DECODE, dev, batch=self.batch,
+                                      num_q_heads=num_q_heads, num_kv_heads=num_kv_heads)
         self._pages = None
 
     @classmethod
@@ -320,9 +321,9 @@ class PageManager:
         self.pools, self.page_table, self.seq_lens = pools, page_table, seq_lens
         self.device, self.num_phys_pages = dev, p_phys
         self.batch, self.max_pages = page_table.shape
+        self.num_used = torch.zeros((), dtype=torch.int32, device=dev)
         self.ws = twl.alloc_workspace(twl.TWL_OP_PAGES, dev, batch=self.batch,
                                       max_pages=self.max_pages, rows=p_phys)
-        self.num_used = torch.zeros((), dtype=torch.int32, device=dev)
 
     def remap(self, parent, reserve=None, sinks: int = 0, window: int = ALL_TOKENS,
               stream=None) -> None:

@@ -227,11 +227,16 @@ def twl_device_status(ws, clear: bool = False, stream=None) -> tuple[int, int]:
 
 
 def alloc_workspace(op: int, device, **dims) -> torch.Tensor:
-    """A zero-initialised workspace tensor of twl_workspace_bytes(op, **dims) bytes."""
+    """A zero-initialised workspace tensor of twl_workspace_bytes(op, **dims) bytes.  The zeros are
+    there when this returns, so a call on any stream may use it (within a capture they are a node
+    of the graph, before the calls captured behind it)."""
     n = twl_workspace_bytes(op, **dims)
     if n == 0:
         raise TwlError(TWL_ERR_INVALID_ARG, "twl_workspace_bytes")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    ws = torch.zeros(n, dtype=torch.uint8, device=device)
+    if ws.is_cuda and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(ws.device).synchronize()
+    return ws
 
 
 def twl_page_bounds(kv: PagedKV, bounds, ws=None, stream=None) -> None:

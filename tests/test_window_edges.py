@@ -1,10 +1,12 @@
 """Windowed attention and the 4-bit cache where calls and kernels meet: repeated launches, rows that
 are not finite, streams, workspaces, limits.  Helpers and tolerances are those of test_window.py."""
+import contextlib
 import math
 
 import pytest
 import torch
 
+from adaptive_top_sparse_b200 import twl
 from test_window import ALL, D, PAGE, _attend, _check, _deal, _rand, _rows, _seen
 
 
@@ -80,3 +82,60 @@ def test_a_score_that_is_not_finite_counts_at_every_key(bad, where, qn, copies):
             _check(one[c][~near[-1]], lse1[c][~near[-1]], want[-1][~near[-1]], wlse[-1][~near[-1]],
                    6.0, whole[2], False)
         assert layer.status() == (0, 0)
+
+
+# ------------------------------------------------------------------ streams
+class _FakeStream:
+    def __init__(self, device=None):
+        self.device, self.waits = device, 0
+
+    def synchronize(self):
+        self.waits += 1
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_a_workspace_is_zero_when_it_is_handed_out(monkeypatch, capturing):
+    """Without a GPU: alloc_workspace waits for its zeros, except within a capture."""
+    class Zeros:
+        is_cuda, device = True, "a device"
+    stream, order = _FakeStream("a device"), []
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: order.append(stream.waits) or Zeros())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: stream)
+    ws = twl.alloc_workspace(twl.TWL_OP_PAGES, "cuda", batch=1, max_pages=1, rows=1)
+    assert isinstance(ws, Zeros) and order == [0]
+    assert stream.waits == (0 if capturing else 1)
+
+
+@contextlib.contextmanager
+def _busy():
+    """The current stream has about 0.2 s of work queued while the body runs."""
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)
+    yield
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_a_manager_made_on_a_busy_stream_serves_another():
+    """A manager, its layer and a 4-bit layer are made while the current stream is busy; their first
+    calls, on another stream, give what calls in order give."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer, Int4Layer
+    side, got = torch.cuda.Stream(), []
+    for busy in (False, True):
+        table, n, pages = _deal([300, 45, 2000], 3, extra_pages=2, spare=8)
+        k, v = _rand(1, pages, 2, PAGE, D), _rand(2, pages, 2, PAGE, D)
+        kn, q = _rand(3, 3, 2, D), _rand(4, 3, 8, D)
+        codes = (torch.arange(2 * pages * 2 * PAGE * 64, device="cuda") % 251).to(torch.uint8)
+        codes = codes.view(2, pages, 2, PAGE, 64)
+        sz = _rand(5, 2, pages, 2, PAGE, 2).abs()
+        parent = torch.tensor([0, 0, 2], dtype=torch.int32, device="cuda")
+        with _busy() if busy else contextlib.nullcontext():
+            stream = side if busy else None
+            four = Int4Layer(codes[0], sz[0], codes[1], sz[1], table.clone(), n.clone(), 8, 2)
+            four.pages().remap(parent, parent, stream=stream)
+            four.decode(q, kn, kn, 4, 100, stream=stream)
+            side.synchronize()
+            out = [x.clone() for x in (four.page_table, four.seq_lens, four.k, four.o, four.lse)]
+        got.append(out)
+    assert all(torch.equal(x, y) for x, y in zip(*got))
