@@ -9,6 +9,7 @@ is a call into libtwl.so.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
@@ -50,6 +51,17 @@ def on_device(device, call, *args) -> None:
     else:
         with torch.cuda.device(device):
             call(*args)
+
+
+def launch_stream(device, stream):
+    """A context in which `stream` (a torch stream or a raw handle) is the current one: what is
+    allocated and filled there is ordered before a launch on it.  None is the current stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
+            torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 class DecodeLayer:
@@ -158,25 +170,32 @@ class DecodeLayer:
                        stream=None):
         """Chunks of many tokens: rows q_start[b] .. q_start[b + 1] - 1 of q [T][Hq][128] fp16 are
         the last tokens of sequence b (already in its cache) and attend causally under the window.
-        Returns (o fp16 [T][Hq][128], lse fp32 [T][Hq]), new tensors or the pair `out`; rows
-        outside every chunk are not written."""
+        Returns (o fp16 [T][Hq][128], lse fp32 [T][Hq]), new tensors (made on the launch's stream)
+        or the pair `out`; rows outside every chunk are not written."""
         dev = self.k.device
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q: expected a tensor [T][Hq][128]")
         expect_tensor("q", q, (q.shape[0], self.num_q_heads, 128), torch.float16, dev)
         expect_tensor("q_start", q_start, (self.batch + 1,), torch.int32, dev)
         if out is None:
-            out = (torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device=dev))
+            with launch_stream(dev, stream):
+                out = (torch.empty_like(q),
+                       torch.empty(q.shape[:2], dtype=torch.float32, device=dev))
+                capturing = torch.cuda.is_current_stream_capturing()
+            if stream is not None and not capturing:
+                for t in out:                  # the caller reads them on the current stream
+                    t.record_stream(torch.cuda.current_stream(dev))
         o, lse = out
         expect_tensor("o", o, q.shape, torch.float16, dev)
         expect_tensor("lse", lse, q.shape[:2], torch.float32, dev)
         if self.ws_prefill is None:
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("window_prefill: the layer's first call makes its workspace, "
-                                   "so it cannot be captured")
-            self.ws_prefill = twl.alloc_workspace(
-                twl.TWL_OP_WINDOW_PREFILL, dev, batch=self.batch, num_q_heads=self.num_q_heads,
-                num_kv_heads=self.num_kv_heads)
+            with launch_stream(dev, stream):
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("window_prefill: the layer's first call makes its "
+                                       "workspace, so it cannot be captured")
+                self.ws_prefill = twl.alloc_workspace(
+                    twl.TWL_OP_WINDOW_PREFILL, dev, batch=self.batch,
+                    num_q_heads=self.num_q_heads, num_kv_heads=self.num_kv_heads)
         on_device(dev, twl.twl_window_prefill, q, q_start, q.shape[0], self.num_q_heads, self.kv,
                   sinks, window, SM_SCALE, o, lse, self.ws_prefill, stream)
         return o, lse

@@ -139,3 +139,69 @@ def test_a_manager_made_on_a_busy_stream_serves_another():
             out = [x.clone() for x in (four.page_table, four.seq_lens, four.k, four.o, four.lse)]
         got.append(out)
     assert all(torch.equal(x, y) for x, y in zip(*got))
+
+
+def test_chunks_make_their_outputs_and_workspace_on_the_launch_stream(monkeypatch):
+    """Without a GPU, on meta tensors: what window_prefill allocates is allocated with the launch's
+    stream current, and its first call is refused when that stream is being captured."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer
+    now, seen = ["current"], []
+
+    @contextlib.contextmanager
+    def stream_context(stream):
+        now.append(stream)
+        try:
+            yield
+        finally:
+            now.pop()
+    empty, empty_like = torch.empty, torch.empty_like
+    monkeypatch.setattr(torch.cuda, "stream", stream_context)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: now[-1])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now[-1] == "captured")
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: seen.append(("record", s)))
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: seen.append(("o", now[-1])) or empty(*a, **k))
+    monkeypatch.setattr(torch, "empty_like",
+                        lambda *a, **k: seen.append(("o", now[-1])) or empty_like(*a, **k))
+    monkeypatch.setattr(twl, "alloc_workspace", lambda *a, **k: seen.append(("ws", now[-1])) or "ws")
+    monkeypatch.setattr(twl, "twl_window_prefill",
+                        lambda *a: seen.append(("launch", a[-1], a[-2], now[-1])))
+    q = empty((5, 8, 128), dtype=torch.float16, device="meta")
+    start = empty((4,), dtype=torch.int32, device="meta")
+    out = (empty_like(q), empty((5, 8), dtype=torch.float32, device="meta"))
+    layer = DecodeLayer.__new__(DecodeLayer)
+    layer.k, layer.kv = empty((4, 2, 16, 128), dtype=torch.float16, device="meta"), None
+    layer.batch, layer.num_q_heads, layer.num_kv_heads, layer.ws_prefill = 3, 8, 2, None
+    with pytest.raises(RuntimeError):
+        layer.window_prefill(q, start, out=out, stream="captured")
+    assert seen == [] and layer.ws_prefill is None
+    layer.window_prefill(q, start, stream="side")
+    assert sorted(seen[:2]) == [("o", "side")] * 2 and ("ws", "side") in seen
+    assert seen.count(("record", "current")) == 2
+    assert seen[-1] == ("launch", "side", "ws", "current")
+    seen.clear()
+    layer.window_prefill(q, start, out=out, stream="captured")
+    assert seen == [("launch", "captured", "ws", "current")]
+    seen.clear()
+    layer.window_prefill(q, start)
+    assert seen == [("o", "current")] * 2 + [("launch", None, "ws", "current")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("raw", [False, True])        # the stream, or its handle
+def test_first_chunks_on_another_stream_than_the_busy_one(raw):
+    from adaptive_top_sparse_b200.layer import DecodeLayer
+    lens, qn = [3000, 700, 40], [900, 300, 40]
+    table, n, pages = _deal(lens, 3)
+    k, v = _rand(1, pages, 2, PAGE, D), _rand(2, pages, 2, PAGE, D)
+    start = torch.tensor([0] + qn).cumsum(0).int().cuda()
+    q = _rand(3, sum(qn), 8, D)
+    want = [x.clone() for x in DecodeLayer(k, v, table, n, 8, 2).window_prefill(q, start, 4, 500)]
+    side = torch.cuda.Stream()
+    layer = DecodeLayer(k, v, table, n, 8, 2)
+    with _busy():
+        got = layer.window_prefill(q, start, 4, 500, stream=side.cuda_stream if raw else side)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert layer.status() == (0, 0)
