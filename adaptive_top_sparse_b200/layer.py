@@ -269,22 +269,23 @@ class Int4Layer:
     def from_fp16(cls, k, v, page_table, seq_lens, num_q_heads: int, num_kv_heads: int,
                   stream=None):
         """The layer of an fp16 cache (device tensors, layout of DecodeLayer): quantises K and V
-        of every page the sequences use."""
+        of every page the sequences use, on `stream`, where the layer's buffers are made too."""
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise ValueError("k: expected a tensor [P][Hkv][16][128]")
         dev, p_phys = k.device, k.shape[0]
         for name, t in (("k", k), ("v", v)):
             expect_tensor(name, t, (p_phys, num_kv_heads, 16, 128), torch.float16, dev)
         expect_table(page_table, seq_lens, dev)
-        made = []
-        for x in (k, v):
-            codes = torch.zeros((p_phys, num_kv_heads, 16, 64), dtype=torch.uint8, device=dev)
-            sz = torch.zeros((p_phys, num_kv_heads, 16, 2), dtype=torch.float16, device=dev)
-            on_device(dev, twl.twl_quantize_k, twl.PagedKV(x, x, page_table, seq_lens,
-                                                           num_kv_heads, p_phys),
-                      codes, sz, None, stream)
-            made += [codes, sz]
-        return cls(*made, page_table, seq_lens, num_q_heads, num_kv_heads)
+        with launch_stream(dev, stream):      # the zeros before the rows, on one stream
+            made = []
+            for x in (k, v):
+                codes = torch.zeros((p_phys, num_kv_heads, 16, 64), dtype=torch.uint8, device=dev)
+                sz = torch.zeros((p_phys, num_kv_heads, 16, 2), dtype=torch.float16, device=dev)
+                on_device(dev, twl.twl_quantize_k, twl.PagedKV(x, x, page_table, seq_lens,
+                                                               num_kv_heads, p_phys),
+                          codes, sz, None, stream)
+                made += [codes, sz]
+            return cls(*made, page_table, seq_lens, num_q_heads, num_kv_heads)
 
     def decode(self, q, k_new=None, v_new=None, sinks: int = 0, window: int = ALL_TOKENS,
                advance: bool = True, stream=None):

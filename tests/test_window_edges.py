@@ -205,3 +205,46 @@ def test_first_chunks_on_another_stream_than_the_busy_one(raw):
             assert all(torch.equal(x, y) for x, y in zip(want, got))
     assert all(torch.equal(x, y) for x, y in zip(want, got))
     assert layer.status() == (0, 0)
+
+
+def test_a_4_bit_cache_is_filled_and_quantised_on_one_stream(monkeypatch):
+    """Without a GPU, on meta tensors: from_fp16 fills its codes with the stream current that the
+    quantiser runs on."""
+    from adaptive_top_sparse_b200.layer import Int4Layer
+    now, seen = ["current"], []
+
+    @contextlib.contextmanager
+    def stream_context(stream):
+        now.append(stream)
+        try:
+            yield
+        finally:
+            now.pop()
+    zeros = torch.zeros
+    monkeypatch.setattr(torch.cuda, "stream", stream_context)
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: seen.append(now[-1]) or zeros(*a, **k))
+    monkeypatch.setattr(twl, "alloc_workspace", lambda *a, **k: seen.append(now[-1]))
+    monkeypatch.setattr(twl, "twl_quantize_k", lambda *a: seen.append(a[-1]))
+    k = torch.empty((4, 2, 16, 128), dtype=torch.float16, device="meta")
+    table = torch.empty((3, 5), dtype=torch.int32, device="meta")
+    Int4Layer.from_fp16(k, k, table, table[:, 0].clone(), 8, 2, stream="side")
+    assert len(seen) == 9 and set(seen) == {"side"}      # K and V; o, lse and the workspace
+
+
+@pytest.mark.gpu
+def test_a_4_bit_cache_made_on_another_stream_than_the_busy_one():
+    from adaptive_top_sparse_b200.layer import Int4Layer
+    table, n, pages = _deal([3000, 700, 40], 3)
+    k, v, q = _rand(1, pages, 2, PAGE, D), _rand(2, pages, 2, PAGE, D), _rand(3, 3, 8, D)
+    ref = Int4Layer.from_fp16(k, v, table, n, 8, 2)
+    want = [x.clone() for x in (*ref.decode(q), ref.k, ref.k_sz, ref.v, ref.v_sz)]
+    side = torch.cuda.Stream()
+    with _busy():
+        four = Int4Layer.from_fp16(k, v, table, n, 8, 2, stream=side)
+        o, lse = four.decode(q, stream=side)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            got = [x.clone() for x in (o, lse, four.k, four.k_sz, four.v, four.v_sz)]
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert all(torch.equal(x, y) for x, y in
+               zip(want, (four.o, four.lse, four.k, four.k_sz, four.v, four.v_sz)))
