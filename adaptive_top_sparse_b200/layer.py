@@ -43,14 +43,13 @@ def expect_tensor(name: str, t, shape, dtype, device) -> None:
 ALL_TOKENS = 2 ** 31 - 1        # a window of every token
 
 
-def on_device(device, call, *args) -> None:
+def on_device(device, call, *args):
     """call(*args) with `device` current: a stream of None is then that device's current stream,
     and the launch goes there whatever device the caller has current."""
     if device.index is None or device.index == torch.cuda.current_device():
-        call(*args)
-    else:
-        with torch.cuda.device(device):
-            call(*args)
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
 
 
 def launch_stream(device, stream):
@@ -223,9 +222,10 @@ class DecodeLayer:
             self._double_p = DoubleP(self)
         return self._double_p
 
-    def status(self, clear: bool = False):
-        """(status, flags) of the layer's device flags, over all of its workspaces."""
-        got = [twl.twl_device_status(ws, clear)
+    def status(self, clear: bool = False, stream=None):
+        """(status, flags) of the layer's device flags, over all of its workspaces, behind the
+        calls issued on `stream`, which it waits for."""
+        got = [on_device(self.device, twl.twl_device_status, ws, clear, stream)
                for ws in (self.ws, self.ws_window, self.ws_prefill) if ws is not None]
         return next((st for st, _ in got if st != twl.TWL_OK), twl.TWL_OK), \
             got[0][1] | got[1][1] | (got[2][1] if len(got) > 2 else 0)
@@ -312,8 +312,10 @@ class Int4Layer:
                                       self.seq_lens)
         return self._pages
 
-    def status(self, clear: bool = False):
-        return twl.twl_device_status(self.ws, clear)
+    def status(self, clear: bool = False, stream=None):
+        """(status, flags) of the device flags, behind the calls issued on `stream`, which it
+        waits for."""
+        return on_device(self.device, twl.twl_device_status, self.ws, clear, stream)
 
 
 def expect_table(page_table, seq_lens, device) -> None:
@@ -368,8 +370,10 @@ class PageManager:
                   self.num_phys_pages, self.num_used, self.ws, stream)
         return self.num_used
 
-    def status(self, clear: bool = False):
-        return twl.twl_device_status(self.ws, clear)
+    def status(self, clear: bool = False, stream=None):
+        """(status, flags) of the device flags, behind the calls issued on `stream`, which it
+        waits for."""
+        return on_device(self.device, twl.twl_device_status, self.ws, clear, stream)
 
 
 class DoubleP:

@@ -248,3 +248,42 @@ def test_a_4_bit_cache_made_on_another_stream_than_the_busy_one():
     assert all(torch.equal(x, y) for x, y in zip(want, got))
     assert all(torch.equal(x, y) for x, y in
                zip(want, (four.o, four.lse, four.k, four.k_sz, four.v, four.v_sz)))
+
+
+def test_status_reads_behind_the_stream_it_is_given(monkeypatch):
+    from adaptive_top_sparse_b200.layer import DecodeLayer, Int4Layer, PageManager
+    seen = []
+    monkeypatch.setattr(twl, "twl_device_status",
+                        lambda ws, clear, stream: seen.append((ws, clear, stream)) or (0, 0))
+    for cls, spaces in ((DecodeLayer, ("ws", "ws_window", "ws_prefill")), (Int4Layer, ("ws",)),
+                        (PageManager, ("ws",))):
+        one = cls.__new__(cls)
+        one.device = torch.device("meta")
+        for name in spaces:
+            setattr(one, name, name)
+        assert one.status(True, stream="side") == (0, 0)
+        assert one.status() == (0, 0)
+        assert seen == [(x, c, s) for c, s in ((True, "side"), (False, None)) for x in spaces]
+        seen.clear()
+
+
+@pytest.mark.gpu
+def test_status_of_calls_on_a_busy_stream():
+    """A bad page met behind 0.2 s of other work on a side stream shows in the status read there."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer, Int4Layer, PageManager
+    table, n, pages = _deal([300, 45], 3)
+    k, v, q = _rand(1, pages, 2, PAGE, D), _rand(2, pages, 2, PAGE, D), _rand(3, 2, 8, D)
+    four = Int4Layer.from_fp16(k, v, table, n, 8, 2)
+    layer, manager = DecodeLayer(k, v, table.clone(), n, 8, 2), PageManager([k, v], table, n)
+    bad = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    table[0, 3], layer.page_table[0, 3] = pages, -1
+    side = torch.cuda.Stream()
+    for what, call in ((layer, lambda: layer.window_decode(q, stream=side)),
+                       (four, lambda: four.decode(q, stream=side)),
+                       (manager, lambda: manager.remap(bad, stream=side))):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400_000_000)
+        call()
+        assert what.status(clear=True, stream=side) == (twl.TWL_ERR_BAD_INDEX, twl.TWL_FLAG_BAD_INDEX)
+        assert what.status(stream=side) == (0, 0)
