@@ -224,7 +224,7 @@ size_t twl_workspace_bytes(int32_t op, int32_t batch, int32_t num_q_heads, int32
     case TWL_OP_WINDOW_DECODE:
     case TWL_OP_INT4_DECODE:
       if (num_kv_heads < 1 || num_q_heads < num_kv_heads) return 0;
-      c.take<char>(window::workspace_bytes(batch, num_q_heads, num_kv_heads));
+      c.take<char>(window::workspace_bytes(num_q_heads, num_kv_heads));
       break;
     case TWL_OP_WINDOW_PREFILL:
       if (num_kv_heads < 1 || num_q_heads < num_kv_heads) return 0;
@@ -232,7 +232,7 @@ size_t twl_workspace_bytes(int32_t op, int32_t batch, int32_t num_q_heads, int32
       break;
     case TWL_OP_PAGES:
       if (rows < 0) return 0;
-      c.take<char>(pages::workspace_bytes(batch, max_pages, rows));
+      c.take<char>(pages::workspace_bytes(batch, max_pages));
       break;
     default:
       return 0;
@@ -567,9 +567,9 @@ twl_status twl_window_decode(const void* q, int32_t num_q_heads, const twl_paged
   if ((st = check_window(sinks, window, sm_scale)) != TWL_OK) return st;
   if (!q || !o || !lse || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4))
     return TWL_ERR_INVALID_ARG;
-  if ((long long)k.batch * k.hkv > 4096) return TWL_ERR_UNSUPPORTED;
+  if ((long long)k.batch * k.hkv > kWindowGroups) return TWL_ERR_UNSUPPORTED;
   Carve c{static_cast<char*>(ws)};
-  void* body = c.take<char>(window::workspace_bytes(k.batch, num_q_heads, k.hkv));
+  void* body = c.take<char>(window::workspace_bytes(num_q_heads, k.hkv));
   if ((st = check_ws(ws, ws_bytes, c.off)) != TWL_OK) return st;
   window::Args a = {};
   a.q = static_cast<const uint16_t*>(q);
@@ -606,7 +606,7 @@ twl_status twl_window_prefill(const void* q, const int32_t* q_start, int32_t tot
   if (total_q < 0 || !q_start || !aligned(q_start, 4)) return TWL_ERR_INVALID_ARG;
   if (total_q > 0 && (!q || !o || !lse || !aligned(q, 16) || !aligned(o, 32) || !aligned(lse, 4)))
     return TWL_ERR_INVALID_ARG;
-  if ((long long)k.batch * k.hkv > 4096) return TWL_ERR_UNSUPPORTED;
+  if ((long long)k.batch * k.hkv > kWindowGroups) return TWL_ERR_UNSUPPORTED;
   Carve c{static_cast<char*>(ws)};
   void* body = c.take<char>(prefill::workspace_bytes());
   if ((st = check_ws(ws, ws_bytes, c.off)) != TWL_OK) return st;
@@ -653,9 +653,9 @@ twl_status twl_int4_decode(const void* q, int32_t num_q_heads, const twl_int4_kv
     return TWL_ERR_INVALID_ARG;
   if (!k_new != !v_new || (advance && !k_new) || !aligned(k_new, 16) || !aligned(v_new, 16))
     return TWL_ERR_INVALID_ARG;
-  if ((long long)k.batch * k.hkv > 4096) return TWL_ERR_UNSUPPORTED;
+  if ((long long)k.batch * k.hkv > kWindowGroups) return TWL_ERR_UNSUPPORTED;
   Carve c{static_cast<char*>(ws)};
-  void* body = c.take<char>(window::workspace_bytes(k.batch, num_q_heads, k.hkv));
+  void* body = c.take<char>(window::workspace_bytes(num_q_heads, k.hkv));
   if ((st = check_ws(ws, ws_bytes, c.off)) != TWL_OK) return st;
   window::Args a = {};
   a.q = static_cast<const uint16_t*>(q);
@@ -697,7 +697,7 @@ twl_status twl_remap_pages(const twl_page_pool* pools, int32_t num_pools, int32_
       !aligned(reserve, 4) || sinks < 0 || window < 1)
     return TWL_ERR_INVALID_ARG;
   Carve c{static_cast<char*>(ws)};
-  void* body = c.take<char>(pages::workspace_bytes(batch, max_pages, num_phys_pages));
+  void* body = c.take<char>(pages::workspace_bytes(batch, max_pages));
   if ((st = check_ws(ws, ws_bytes, c.off)) != TWL_OK) return st;
   pages::Args a = {};
   a.table = page_table;
@@ -725,7 +725,7 @@ twl_status twl_compact_pages(const twl_page_pool* pools, int32_t num_pools,
   if (!page_table_out || !num_used || !aligned(page_table_out, 4) || !aligned(num_used, 4))
     return TWL_ERR_INVALID_ARG;
   Carve c{static_cast<char*>(ws)};
-  void* body = c.take<char>(pages::workspace_bytes(batch, max_pages, num_phys_pages));
+  void* body = c.take<char>(pages::workspace_bytes(batch, max_pages));
   if ((st = check_ws(ws, ws_bytes, c.off)) != TWL_OK) return st;
   pages::Args a = {};
   a.table = const_cast<int*>(page_table);  // read only unless it is page_table_out

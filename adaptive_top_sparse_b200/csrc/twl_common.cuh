@@ -13,6 +13,11 @@ constexpr int kHeadDim = 128;
 constexpr int kPage = 16;
 constexpr int kHeaderBytes = 256;
 constexpr int kMaxPages = 32768;
+// Attention under a window: (sequence, kv-head) groups of a call, and the words at the start of its
+// workspace that are zero between launches.  The same place and size for every shape and call, so
+// that one workspace serves them all.
+constexpr int kWindowGroups = 4096;
+constexpr int kCounterWords = kWindowGroups + 64;
 
 // Workspace header: word 0 = sticky device flags (TWL_FLAG_*); the rest is reserved.
 struct WsHeader {

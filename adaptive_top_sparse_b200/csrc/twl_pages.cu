@@ -426,15 +426,16 @@ cudaError_t launch(const void* kernel, const Args& a, const Pools& p, size_t sme
 
 }  // namespace
 
-size_t workspace_bytes(int batch, int max_pages, int num_phys) {
-  return kSyncWords * 4 + (size_t)groups_of(num_phys) * kGroupWords * 4 +
-         (size_t)batch * max_pages * 4 + (size_t)batch * 16;
+// The bitmap has room for the largest pool: what is zero between launches lies in one place whatever
+// the call's sizes, so that one workspace serves them all.
+size_t workspace_bytes(int batch, int max_pages) {
+  return kSyncWords * 4 + kMaxPool / 8 + (size_t)batch * max_pages * 4 + (size_t)batch * 16;
 }
 
 void carve(Args& a, void* ws) {
   a.sync = static_cast<unsigned*>(ws);
   a.bitmap = a.sync + kSyncWords;  // 16-byte aligned: read as uint4
-  a.next = reinterpret_cast<int*>(a.bitmap + (size_t)groups_of(a.num_phys) * kGroupWords);
+  a.next = reinterpret_cast<int*>(a.bitmap + kMaxPool / 32);
   a.slot = a.next + (size_t)a.batch * a.max_pages;
 }
 

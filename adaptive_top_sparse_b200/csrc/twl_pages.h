@@ -36,7 +36,7 @@ struct Args {
   uint32_t* flags;
 };
 
-size_t workspace_bytes(int batch, int max_pages, int num_phys);
+size_t workspace_bytes(int batch, int max_pages);
 void carve(Args& a, void* ws);
 cudaError_t launch_remap(const Args& a, const Pools& p, cudaStream_t s);
 cudaError_t launch_compact(const Args& a, const Pools& p, cudaStream_t s);

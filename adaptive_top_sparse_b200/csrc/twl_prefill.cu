@@ -1157,12 +1157,12 @@ cudaError_t launch_g(const Args& a, cudaStream_t s) {
 }  // namespace
 
 size_t workspace_bytes() {
-  return (size_t)num_sms() * (2 * kPartFloats * sizeof(float) + sizeof(unsigned));
+  return kCounterWords * sizeof(unsigned) + (size_t)num_sms() * 2 * kPartFloats * sizeof(float);
 }
 
 cudaError_t launch(Args a, void* ws, cudaStream_t s) {
-  a.part = static_cast<float*>(ws);
-  a.done = reinterpret_cast<unsigned*>(a.part + (size_t)num_sms() * 2 * kPartFloats);
+  a.done = static_cast<unsigned*>(ws);  // a word per SM: fewer than kCounterWords
+  a.part = reinterpret_cast<float*>(a.done + kCounterWords);
   switch (a.hq / a.hkv) {
     case 1: return launch_g<1>(a, s);
     case 2: return launch_g<2>(a, s);

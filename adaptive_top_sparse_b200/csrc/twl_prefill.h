@@ -22,8 +22,8 @@ struct Args {
   float* lse;        // [total_q][hq]
   uint32_t* flags;
   // workspace, set by launch()
-  float* part;     // [SMs][2][256 rows x 130] partials of units cut by runs
   unsigned* done;  // [SMs] arrived partials, by the run the unit starts in; zero between launches
+  float* part;     // [SMs][2][256 rows x 130] partials of units cut by runs
 };
 
 size_t workspace_bytes();

@@ -856,17 +856,15 @@ cudaError_t launch_g(const Args& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t workspace_bytes(int batch, int hq, int hkv) {
+size_t workspace_bytes(int hq, int hkv) {
   const size_t g = hq / hkv;
-  return (size_t)num_sms() * 2 * g * kPartStride * sizeof(float) +
-         ((size_t)batch * hkv + 1) * sizeof(unsigned);
+  return kCounterWords * sizeof(unsigned) + (size_t)num_sms() * 2 * g * kPartStride * sizeof(float);
 }
 
 void carve(Args& a, void* ws) {
-  const int g = a.hq / a.hkv;
-  a.part = static_cast<float*>(ws);
-  a.done = reinterpret_cast<unsigned*>(a.part + (size_t)num_sms() * 2 * g * kPartStride);
-  a.left = a.done + (size_t)a.batch * a.hkv;
+  a.done = static_cast<unsigned*>(ws);
+  a.left = a.done + kWindowGroups;
+  a.part = reinterpret_cast<float*>(a.done + kCounterWords);
 }
 
 cudaError_t launch(const Args& a, cudaStream_t s) {

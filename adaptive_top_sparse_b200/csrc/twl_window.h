@@ -23,14 +23,14 @@ struct Args {
   float scale_log2;  // score scale * log2(e)
   float* o;
   float* lse;
-  float* part;     // [SMs][2][G][132] partials of groups cut by runs
   unsigned* done;  // [groups] arrived partials; zero between launches
   unsigned* left;  // CTAs that left (advance); zero between launches
+  float* part;     // [SMs][2][G][132] partials of groups cut by runs
   uint32_t* flags;
 };
 
-size_t workspace_bytes(int batch, int hq, int hkv);
-// Points the workspace arrays of `a` (hq, hkv, batch set) into `ws`, behind the header.
+size_t workspace_bytes(int hq, int hkv);
+// Points the workspace arrays of `a` into `ws`, behind the header.
 void carve(Args& a, void* ws);
 cudaError_t launch(const Args& a, cudaStream_t s);
 

@@ -31,7 +31,11 @@
  *   - A workspace is caller-owned device memory of at least twl_workspace_bytes(...) bytes,
  *     256-byte aligned.  Its first 256 bytes are a header that must be zero before first use
  *     (twl_workspace_init).  Workspaces may be reused across calls on the same stream; calls
- *     that run concurrently must not share one.
+ *     that run concurrently must not share one.  A workspace that is to be zeroed as a whole has
+ *     words that each launch leaves zero for the next; between two twl_workspace_init it serves
+ *     one of these groups: twl_decode_step with one set of sizes; twl_window_decode,
+ *     twl_window_prefill and twl_int4_decode of any sizes; twl_remap_pages and twl_compact_pages
+ *     of any sizes (the size it needs is the largest of the calls').
  *   - Supported shapes: head_dim = 128, page_size = 16, num_q_heads / num_kv_heads in
  *     {1, 2, 4, 8}, max_pages <= 32768 (512K tokens per sequence).
  *
@@ -123,7 +127,7 @@ typedef struct twl_step_stats {
 #define TWL_OP_WINDOW_DECODE 9 /* twl_window_decode                         */
 #define TWL_OP_WINDOW_PREFILL 10 /* twl_window_prefill                        */
 #define TWL_OP_INT4_DECODE 11  /* twl_int4_decode                           */
-#define TWL_OP_PAGES 12        /* twl_remap_pages, twl_compact_pages (rows = num_phys_pages) */
+#define TWL_OP_PAGES 12        /* twl_remap_pages, twl_compact_pages (batch, max_pages) */
 size_t twl_workspace_bytes(int32_t op, int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                            int32_t max_pages, int32_t max_budget, int32_t rows,
                            int32_t row_stride);
@@ -434,7 +438,7 @@ twl_status twl_int4_decode(const void* q, int32_t num_q_heads, const twl_int4_kv
  *   page_table_out (may be page_table) gets the table with the new numbers.  An entry
  *   >= num_phys_pages raises TWL_FLAG_BAD_INDEX and nothing is changed.
  * Both: page_table int32 [batch][max_pages], seq_lens int32 [batch], 1 <= num_pools <=
- *   TWL_MAX_POOLS, workspace TWL_OP_PAGES (batch, max_pages, rows = num_phys_pages), zeroed once;
+ *   TWL_MAX_POOLS, workspace TWL_OP_PAGES (batch, max_pages), zeroed once;
  *   batch > 4096 or num_phys_pages > 8388608 (2^23): TWL_ERR_UNSUPPORTED.  One cooperative launch
  *   each (every SM takes one CTA); a wait that gives up raises TWL_FLAG_TIMEOUT (state undefined). */
 #define TWL_MAX_POOLS 128

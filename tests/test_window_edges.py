@@ -287,3 +287,74 @@ def test_status_of_calls_on_a_busy_stream():
         call()
         assert what.status(clear=True, stream=side) == (twl.TWL_ERR_BAD_INDEX, twl.TWL_FLAG_BAD_INDEX)
         assert what.status(stream=side) == (0, 0)
+
+
+# ------------------------------------------------------------------ workspaces
+@pytest.mark.gpu
+def test_one_workspace_serves_attention_of_every_shape():
+    """One token, chunks and a 4-bit cache, groups of 8, 1 and 4 heads and batches of 1 to 40 in turn
+    through one workspace give the bits that each gives in its own."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer, Int4Layer
+    calls = []
+    for i, (hq, hkv, lens, qn) in enumerate([
+            (16, 2, [5000], [60]), (4, 4, [3000, 900], [500, 10]),
+            (8, 2, [100 + 90 * i for i in range(40)], [1 + 3 * i for i in range(40)]),
+            (8, 1, [9000, 17], [300, 17]), (1, 1, [20000], [1])]):
+        table, n, pages = _deal(lens, i)
+        k, v = _rand(1, pages, hkv, PAGE, D), _rand(2, pages, hkv, PAGE, D)
+        layer, four = DecodeLayer(k, v, table, n, hq, hkv), Int4Layer.from_fp16(k, v, table, n, hq, hkv)
+        q, qp = _rand(3, len(lens), hq, D), _rand(4, sum(qn), hq, D)
+        start = torch.tensor([0] + qn).cumsum(0).int().cuda()
+        for call in (lambda l=layer, q=q: l.window_decode(q, 4, 10000),
+                     lambda l=layer, q=qp, s=start: l.window_prefill(q, s, 4, 3000),
+                     lambda l=four, q=q: l.decode(q)):
+            calls.append((call, [x.clone() for x in call()], layer, four))
+    shared = twl.alloc_workspace(twl.TWL_OP_WINDOW_PREFILL, "cuda", batch=1, num_q_heads=1,
+                                 num_kv_heads=1)
+    for _, _, layer, four in calls:
+        layer.ws_window = layer.ws_prefill = four.ws = shared
+    for order in (calls, calls[::-1], calls):
+        for call, want, layer, four in order:
+            for x in (layer.o, layer.lse, four.o, four.lse):
+                x.fill_(math.nan)
+            assert all(torch.equal(x, y) for x, y in zip(call(), want))
+    assert twl.twl_device_status(shared) == (0, 0)
+
+
+@pytest.mark.gpu
+def test_one_workspace_serves_pools_and_tables_of_every_size():
+    """Page steps and compactions of small and large pools and tables in turn through one workspace
+    give what each gives in its own."""
+    from adaptive_top_sparse_b200.layer import PageManager
+    sides = []
+    for lens, spare in (([40, 17], 6), ([4000, 30000], 60000), ([300] * 50, 900), ([5], 30)):
+        for shared in (False, True):
+            table, n, pages = _deal(lens, 7, extra_pages=2, spare=spare)
+            pool = torch.arange(pages * 4, dtype=torch.int32, device="cuda").view(pages, 4)
+            sides.append((shared, PageManager([pool], table, n),
+                          torch.arange(len(lens), dtype=torch.int32, device="cuda") // 2))
+    ws = max((m.ws for _, m, _ in sides), key=lambda t: t.nbytes)
+    ws = torch.zeros_like(ws)
+    for shared, m, _ in sides:
+        if shared:
+            m.ws = ws
+    for step in range(4):
+        for part in (False, True):
+            for shared, m, parent in sides[::-1] if step % 2 else sides:
+                if shared == part:
+                    m.remap(parent, parent, 4, 2000)
+                    m.compact()
+        for (_, a, _), (_, b, _) in zip(sides[::2], sides[1::2]):
+            assert torch.equal(a.page_table, b.page_table) and torch.equal(a.pools[0], b.pools[0])
+            assert torch.equal(a.seq_lens, b.seq_lens) and int(a.num_used) == int(b.num_used)
+            assert a.status() == (0, 0) and b.status() == (0, 0)
+
+
+def test_workspaces_keep_their_zeroed_words_in_one_place():
+    """The words that a launch leaves zero for the next lie before everything whose size depends on
+    the call's: 4096 arrival counters, and a bit for each of 2^23 pages."""
+    wb = twl.twl_workspace_bytes
+    for op in (twl.TWL_OP_WINDOW_DECODE, twl.TWL_OP_INT4_DECODE, twl.TWL_OP_WINDOW_PREFILL):
+        assert wb(op, 1, 1, 1) == wb(op, 64, 8, 8) >= 256 + 4 * 4097
+    assert wb(twl.TWL_OP_PAGES, 1, 0, 0, 1, 0, 1) >= 256 + (1 << 23) // 8
+    assert wb(twl.TWL_OP_PAGES, 4, 0, 0, 64, 0, 16) == wb(twl.TWL_OP_PAGES, 4, 0, 0, 64, 0, 1 << 23)
