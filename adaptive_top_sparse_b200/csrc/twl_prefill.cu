@@ -69,7 +69,7 @@ struct Smem {
   uint64_t q_full, q_free;
   uint64_t full[kBufs], empty[kBufs];
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
-  uint64_t drain;           // an aborted CTA's products in flight
+  uint64_t drain;           // the CTA's products in flight at its end
   uint64_t v_ready[kBufs];  // V of the buffer is loaded and its unseen rows are zero
   uint32_t tmem;
   int aborted;
@@ -595,8 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok && w.next()) {
       if (nseg > 0) ok = warp_wait(sm, &sm.q_free, (nseg - 1) & 1, a.flags);
-      ++nseg;
       if (!ok) break;
+      ++nseg;
       if (lane == 0) {
         bar_expect(&sm.q_full, w.two ? kQBytes : kQBytes / 2);
         for (int x = 0; x < (w.two ? 2 : 1); ++x)
@@ -631,16 +631,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
     }
-    // an aborted CTA leaves only behind its copies in flight
-    if (!ok || dead()) {
-      const long long t0 = clock64();
-      for (int k = max(0, fill - kBufs); k < fill; ++k)
-        while (!bar_try(&sm.full[k % kBufs], (k / kBufs) & 1) && clock64() - t0 < 2000000000ll) {
-        }
-      if (nseg > 0)
-        while (!bar_try(&sm.q_full, (nseg - 1) & 1) && clock64() - t0 < 2000000000ll) {
-        }
-    }
+    // the CTA leaves only behind its copies in flight, whoever gave up and when
+    const long long t0 = clock64();
+    for (int k = max(0, fill - kBufs); k < fill; ++k)
+      while (!bar_try(&sm.full[k % kBufs], (k / kBufs) & 1) && clock64() - t0 < 2000000000ll) {
+      }
+    if (nseg > 0)
+      while (!bar_try(&sm.q_full, (nseg - 1) & 1) && clock64() - t0 < 2000000000ll) {
+      }
   } else if (warp == kMmaWarp) {
     // ================================================================ tensor core
     // One thread walks, waits and issues.  What it does between two products is time the tensor
@@ -785,11 +783,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         w = ahead;
       }
-      if (!ok || dead()) {  // an aborted CTA gives TMEM back only behind its products
-        mma_commit(&sm.drain);
-        const long long t0 = clock64();
-        while (!bar_try(&sm.drain, 0) && clock64() - t0 < 2000000000ll) {
-        }
+      // the CTA gives TMEM back only behind its products, whoever gave up and when
+      mma_commit(&sm.drain);
+      const long long t0 = clock64();
+      while (!bar_try(&sm.drain, 0) && clock64() - t0 < 2000000000ll) {
       }
     }
     __syncwarp();
