@@ -72,6 +72,7 @@ struct Smem {
   uint64_t drain;           // the CTA's products in flight at its end
   uint64_t v_ready[kBufs];  // V of the buffer is loaded and its unseen rows are zero
   uint32_t tmem;
+  uint32_t wait_limit;
   int aborted;
   int rec[kRecs];  // of a key tile: pages that were loaded (bit per page), its number << 8
   int is_last;
@@ -113,11 +114,13 @@ __device__ __forceinline__ bool bar_try_now(uint64_t* b, uint32_t parity) {
       : "=r"(ok) : "r"(sptr(b)), "r"(parity) : "memory");
   return ok != 0;
 }
-constexpr uint32_t kWaitLimit = 1u << 16;  // polls of up to 20 us each
+constexpr uint32_t kWaitLimit = 1u << 16;  // polls of up to 20 us each (Args.wait_limit)
+// An arrival at a cut unit's counter; one of a run that gave up counts in the upper half too.
+constexpr unsigned kArrived = 1u, kGaveUp = 0x10000u;
 
 // Waits for the phase of the given parity; false when the wait, or another in the CTA, gave up.
 __device__ __forceinline__ bool bar_wait(Smem& s, uint64_t* b, uint32_t parity, uint32_t* flags) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+  for (uint32_t i = 0; i < s.wait_limit; ++i) {
     if (bar_try(b, parity)) return true;
     if (*reinterpret_cast<volatile int*>(&s.aborted)) return false;
   }
@@ -485,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == kLoadWarp * 32) {
+    sm.wait_limit = a.wait_limit;
     sm.aborted = 0;
     sm.spoils = 0;
     for (int i = 0; i < kSpoils; ++i) sm.spoil[i].seg = -1;
@@ -710,6 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Walk<G> ahead = w;
       bool more = w.next(), begun = false;
+      // (a test of the waits makes every second run wait for products that nothing issues)
+      if (a.stall && (run & 1)) wait(&sm.drain, 0);
       while (ok && more) {
         if (!begun) first_scores(kb);
         if (!ok) break;
@@ -1043,9 +1049,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 last = run_of(w.start + w.s.tiles - 1, total, runs);
       __threadfence();
       named_sync(1, 512);
-      if (tid == 0)
-        sm.is_last = !dead() && (first == last ||
-                                 atomicAdd(a.done + first, 1u) == (unsigned)(last - first));
+      // A run that gave up arrives too, so that the counter is zero again for the next launch; the
+      // rows of its units are not written.
+      if (tid == 0) {
+        bool merge = !dead();
+        if (first != last) {
+          const unsigned before = atomicAdd(a.done + first, merge ? kArrived : kArrived + kGaveUp);
+          const bool all = (before & (kGaveUp - 1)) == (unsigned)(last - first);
+          if (all) a.done[first] = 0u;
+          merge = merge && all && before < kGaveUp;
+        }
+        sm.is_last = merge;
+      }
       named_sync(1, 512);
       if (sm.is_last) {
         __threadfence();
@@ -1089,7 +1104,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                          pack_half2(__float2half_rn(o.z * inv), __float2half_rn(o.w * inv)));
           if (c == 0) a.lse[dst] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
         }
-        if (tid == 0 && first != last) a.done[first] = 0u;
       }
       named_sync(1, 512);
     }
@@ -1153,6 +1167,16 @@ cudaError_t launch_g(const Args& a, cudaStream_t s) {
 
 }  // namespace
 
+namespace {
+uint32_t g_wait_limit = kWaitLimit;  // test knobs (twl_test_set_waits)
+int g_stall = 0;
+}  // namespace
+
+void set_test_waits(uint32_t max_polls, int stall) {
+  g_wait_limit = max_polls > 0 ? max_polls : kWaitLimit;
+  g_stall = stall != 0;
+}
+
 size_t workspace_bytes() {
   return kCounterWords * sizeof(unsigned) + (size_t)num_sms() * 2 * kPartFloats * sizeof(float);
 }
@@ -1160,6 +1184,8 @@ size_t workspace_bytes() {
 cudaError_t launch(Args a, void* ws, cudaStream_t s) {
   a.done = static_cast<unsigned*>(ws);  // a word per SM: fewer than kCounterWords
   a.part = reinterpret_cast<float*>(a.done + kCounterWords);
+  a.wait_limit = g_wait_limit;
+  a.stall = g_stall;
   switch (a.hq / a.hkv) {
     case 1: return launch_g<1>(a, s);
     case 2: return launch_g<2>(a, s);

@@ -21,12 +21,16 @@ struct Args {
   uint16_t* o;       // [total_q][hq][128]
   float* lse;        // [total_q][hq]
   uint32_t* flags;
+  uint32_t wait_limit;  // polls before a wait gives up
+  int stall;            // test of the waits: every second run's products never start
   // workspace, set by launch()
   unsigned* done;  // [SMs] arrived partials, by the run the unit starts in; zero between launches
   float* part;     // [SMs][2][256 rows x 130] partials of units cut by runs
 };
 
 size_t workspace_bytes();
+// Test knobs for the bounded waits (twl_test_set_waits).
+void set_test_waits(uint32_t max_polls, int stall);
 cudaError_t launch(Args a, void* ws, cudaStream_t s);
 
 }  // namespace prefill

@@ -363,6 +363,8 @@ twl_status twl_sparse_decode_noalloc(const void* q, int32_t num_q_heads, const t
  *   fine.  A sequence whose chunk is not inside [0, total_q] or longer than its length, or whose
  *   length is > 16 * max_pages, is skipped (its outputs are not written), and a page that is out
  *   of range is skipped, both with TWL_FLAG_BAD_INDEX.  total_q = 0 launches nothing.
+ *   A wait inside the kernel that gives up raises TWL_FLAG_TIMEOUT: some rows are not written then;
+ *   the next launch on the workspace is valid.
  *   Workspace TWL_OP_WINDOW_PREFILL (batch, num_q_heads, num_kv_heads), zeroed once.
  *   batch * num_kv_heads > 4096 or num_phys_pages * num_kv_heads >= 2^27: TWL_ERR_UNSUPPORTED. */
 twl_status twl_window_decode(const void* q, int32_t num_q_heads, const twl_paged_kv* kv,
@@ -490,13 +492,15 @@ twl_status twl_decode_step(const void* q, int32_t num_q_heads, const twl_paged_k
                            twl_stream_t stream);
 
 /* ---------------------------------------------------------------- test hook of the bounded waits
- * twl_decode_step's work items wait for one another by polling counters in the workspace; each
- * wait gives up after a bounded number of polls, raises TWL_FLAG_TIMEOUT and aborts the launch
- * (the kernel returns; the context stays usable; the next launch on the workspace is valid).
+ * twl_decode_step's work items wait for one another by polling counters in the workspace, and the
+ * warps of twl_window_prefill for one another in shared memory; each wait gives up after a bounded
+ * number of polls, raises TWL_FLAG_TIMEOUT and aborts the launch (the kernel returns; the context
+ * stays usable; the next launch on the workspace is valid).
  * This hook exists so that a test can make that happen without a device fault: max_polls sets
- * the polls before a wait gives up for later launches (0 = the default, 2^22), and
- * stall_estimate != 0 makes the INT4-estimate items wait for a count that is never reached.
- * Process-wide, read at each twl_decode_step call; not for production use. */
+ * the polls before a wait gives up for later launches (0 = the defaults, 2^22 and, of up to 20 us
+ * each, 2^16), and stall_estimate != 0 makes the INT4-estimate items, and every second CTA of a
+ * chunk launch, wait for what never happens.
+ * Process-wide, read at each twl_decode_step and twl_window_prefill call; not for production use. */
 void twl_test_set_waits(uint32_t max_polls, int32_t stall_estimate);
 
 #ifdef __cplusplus

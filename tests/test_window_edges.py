@@ -358,3 +358,37 @@ def test_workspaces_keep_their_zeroed_words_in_one_place():
         assert wb(op, 1, 1, 1) == wb(op, 64, 8, 8) >= 256 + 4 * 4097
     assert wb(twl.TWL_OP_PAGES, 1, 0, 0, 1, 0, 1) >= 256 + (1 << 23) // 8
     assert wb(twl.TWL_OP_PAGES, 4, 0, 0, 64, 0, 16) == wb(twl.TWL_OP_PAGES, 4, 0, 0, 64, 0, 1 << 23)
+
+
+# ------------------------------------------------------------------ waits that give up
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,lens,qn", [(8, 1, [9000], [2000]), (4, 4, [20000, 300], [5, 300]),
+                                            (8, 8, [400] * 30, [150] * 30)])
+def test_a_chunk_launch_that_gives_up_leaves_a_valid_workspace(hq, hkv, lens, qn):
+    """Through the test hook every second CTA of a chunk launch waits for what never happens: the
+    launch returns with the timeout flag, and the next ones, of the same chunks and of others, are
+    exact, bit for bit those of a layer that never gave up."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer
+    table, n, pages = _deal(lens, 3)
+    k, v = _rand(1, pages, hkv, PAGE, D), _rand(2, pages, hkv, PAGE, D)
+    start = torch.tensor([0] + qn).cumsum(0).int().cuda()
+    q = _rand(3, sum(qn), hq, D)
+    ref = DecodeLayer(k, v, table, n, hq, hkv)
+    want = [[x.clone() for x in ref.window_prefill(q, start, 4, w)] for w in (ALL, 700)]
+    layer = DecodeLayer(k, v, table, n, hq, hkv)
+    out = tuple(torch.empty_like(x) for x in want[0])
+    layer.window_prefill(q, start, 4, ALL, out)
+    for _ in range(2):
+        try:
+            twl.twl_test_set_waits(32, True)
+            layer.window_prefill(q, start, 4, ALL, out)
+            torch.cuda.synchronize()
+        finally:
+            twl.twl_test_set_waits(0, False)
+        assert layer.status(clear=True) == (twl.TWL_ERR_TIMEOUT, twl.TWL_FLAG_TIMEOUT)
+        for i in (0, 1, 0):
+            for x in out:
+                x.fill_(math.nan)
+            layer.window_prefill(q, start, 4, (ALL, 700)[i], out)
+            assert all(torch.equal(x, y) for x, y in zip(want[i], out))
+        assert layer.status() == (0, 0)
