@@ -415,10 +415,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   leave(a, &sh_word);
 }
 
-cudaError_t launch(const void* kernel, const Args& a, const Pools& p, size_t smem,
+size_t remap_smem(int batch, int num_phys) {
+  return (2 * (size_t)batch + 1 + groups_of(num_phys) + 1) * sizeof(int);
+}
+size_t compact_smem(int num_phys) { return ((size_t)groups_of(num_phys) + 1) * sizeof(int); }
+
+// most: the kernel's need for the largest batch and pool.  The attribute is the process's, so every
+// call sets the same value: calls of other host threads never find it below their own need.
+cudaError_t launch(const void* kernel, const Args& a, const Pools& p, size_t smem, size_t most,
                    cudaStream_t s) {
   cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return e;
   void* args[] = {const_cast<Args*>(&a), const_cast<Pools*>(&p)};
   return cudaLaunchCooperativeKernel(kernel, dim3(num_sms()), dim3(kThreads), args, smem, s);
@@ -440,13 +447,13 @@ void carve(Args& a, void* ws) {
 }
 
 cudaError_t launch_remap(const Args& a, const Pools& p, cudaStream_t s) {
-  const size_t smem = (2 * (size_t)a.batch + 1 + groups_of(a.num_phys) + 1) * sizeof(int);
-  return launch(reinterpret_cast<const void*>(k_remap), a, p, smem, s);
+  return launch(reinterpret_cast<const void*>(k_remap), a, p, remap_smem(a.batch, a.num_phys),
+                remap_smem(kMaxBatch, kMaxPool), s);
 }
 
 cudaError_t launch_compact(const Args& a, const Pools& p, cudaStream_t s) {
-  return launch(reinterpret_cast<const void*>(k_compact), a, p,
-                ((size_t)groups_of(a.num_phys) + 1) * sizeof(int), s);
+  return launch(reinterpret_cast<const void*>(k_compact), a, p, compact_smem(a.num_phys),
+                compact_smem(kMaxPool), s);
 }
 
 }  // namespace pages

@@ -846,11 +846,14 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
 
 template <int G, bool INT4>
 cudaError_t launch_g(const Args& a, cudaStream_t s) {
-  const size_t smem = smem_bytes<INT4>(a.batch);
+  // The attribute is the process's: every call sets the largest batch's, so that calls of other host
+  // threads never find it below their own need.
   cudaError_t e = cudaFuncSetAttribute(k_window_decode<G, INT4>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem_bytes<INT4>(kWindowGroups));
   if (e != cudaSuccess) return e;
-  k_window_decode<G, INT4><<<num_sms(), Cfg<INT4>::kWarps * 32, smem, s>>>(a);
+  k_window_decode<G, INT4>
+      <<<num_sms(), Cfg<INT4>::kWarps * 32, smem_bytes<INT4>(a.batch), s>>>(a);
   return cudaGetLastError();
 }
 

@@ -392,3 +392,59 @@ def test_a_chunk_launch_that_gives_up_leaves_a_valid_workspace(hq, hkv, lens, qn
             layer.window_prefill(q, start, 4, (ALL, 700)[i], out)
             assert all(torch.equal(x, y) for x, y in zip(want[i], out))
         assert layer.status() == (0, 0)
+
+
+# ------------------------------------------------------------------ host threads
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", ["decode", "int4", "remap", "compact"])
+def test_host_threads_with_calls_of_different_sizes(call):
+    """Two host threads, each with its own tensors, workspace and stream, one with the smallest
+    shapes and one with large ones: every call launches, and they give what they give alone."""
+    import threading
+    from adaptive_top_sparse_b200.layer import DecodeLayer, Int4Layer, PageManager
+    lib, jobs = twl._lib, []
+    for batch in (1, 4000):
+        table, n, pages = _deal([20] * batch, 3, extra_pages=1, spare=40000 if batch > 1 else 3)
+        stream, same = torch.cuda.Stream(), torch.arange(batch, dtype=torch.int32, device="cuda")
+        if call in ("decode", "int4"):
+            k, v, q = _rand(1, pages, 1, PAGE, D), _rand(2, pages, 1, PAGE, D), _rand(3, batch, 1, D)
+            layer = DecodeLayer(k, v, table, n, 1, 1) if call == "decode" else \
+                Int4Layer.from_fp16(k, v, table, n, 1, 1)
+            ws = layer.ws_window if call == "decode" else layer.ws
+            kv, rest = layer.kv.c(), (0, ALL, 0.1, layer.o.data_ptr(), layer.lse.data_ptr(),
+                                      ws.data_ptr(), ws.nbytes, stream.cuda_stream)
+            fn, args = (lib.twl_window_decode, (q.data_ptr(), 1, kv)) if call == "decode" else \
+                (lib.twl_int4_decode, (q.data_ptr(), 1, kv, None, None, 0))
+            keep, result = (layer, k, v, q), (layer.o, layer.lse)
+        else:
+            manager = PageManager([torch.zeros((pages, 4), dtype=torch.int32, device="cuda")],
+                                  table, n)
+            out = torch.empty_like(table)
+            pools, ws = twl._pools(manager.pools), manager.ws
+            rest = (ws.data_ptr(), ws.nbytes, stream.cuda_stream)
+            fn, args = (lib.twl_remap_pages, (pools, 1, table.data_ptr(), n.data_ptr(), batch,
+                                              table.shape[1], pages, same.data_ptr(), None, 0, ALL)) \
+                if call == "remap" else \
+                (lib.twl_compact_pages, (pools, 1, table.data_ptr(), out.data_ptr(), batch,
+                                         table.shape[1], pages, manager.num_used.data_ptr()))
+            keep, result = (manager, out, pools), (table, n) if call == "remap" else (out,)
+        assert fn(*args, *rest) == 0
+        torch.cuda.synchronize()
+        jobs.append((fn, args + rest, stream, keep, result, [x.clone() for x in result]))
+    failed = []
+
+    def loop(fn, args, stream):
+        for i in range(4000):
+            if fn(*args) != 0:
+                failed.append(i)
+            if i % 100 == 99:
+                stream.synchronize()
+    threads = [threading.Thread(target=loop, args=job[:3]) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == []
+    for job in jobs:
+        assert all(torch.equal(x, y) for x, y in zip(job[4], job[5]))
