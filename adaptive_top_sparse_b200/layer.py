@@ -329,6 +329,7 @@ def expect_table(page_table, seq_lens, device) -> None:
 class PageManager:
     """The pages of one page table and of every pool (tensor [num_phys_pages][...]) it indexes:
     the K and V of one layer, or of all layers that share the table.  Uses the tensors in place.
+    A pool's page is a multiple of 16 bytes, 16-byte aligned; any number of pools will do.
     A page is in use when the table names it; nothing else is kept.  Issue the calls in order on
     one stream, the one that the attention calls on the same cache use."""
 
@@ -339,11 +340,18 @@ class PageManager:
         dev, p_phys = pools[0].device, pools[0].shape[0]
         for t in pools:
             expect_tensor("pool", t, (p_phys, *t.shape[1:]), t.dtype, dev)
+            if t.nbytes == 0 or t.nbytes // p_phys % 16 or (dev.type != "meta" and t.data_ptr() % 16):
+                raise ValueError("pool: expected pages of a multiple of 16 bytes, 16-byte aligned, "
+                                 f"got {t.nbytes} bytes in {p_phys} pages")
         expect_table(page_table, seq_lens, dev)
         self.pools, self.page_table, self.seq_lens = pools, page_table, seq_lens
         self.device, self.num_phys_pages = dev, p_phys
         self.batch, self.max_pages = page_table.shape
         self.num_used = torch.zeros((), dtype=torch.int32, device=dev)
+        # table and lengths that the calls for pools behind the first TWL_MAX_POOLS work on
+        self._copies = None
+        if len(pools) > twl.TWL_MAX_POOLS:
+            self._copies = torch.empty_like(page_table), torch.empty_like(seq_lens)
         self.ws = twl.alloc_workspace(twl.TWL_OP_PAGES, dev, batch=self.batch,
                                       max_pages=self.max_pages, rows=p_phys)
 
@@ -356,8 +364,16 @@ class PageManager:
         expect_tensor("parent", parent, (self.batch,), torch.int32, self.device)
         if reserve is not None:
             expect_tensor("reserve", reserve, (self.batch,), torch.int32, self.device)
-        on_device(self.device, twl.twl_remap_pages, self.pools, self.page_table, self.seq_lens,
-                  self.num_phys_pages, parent, reserve, sinks, window, self.ws, stream)
+        def step(pools, table, lens):
+            on_device(self.device, twl.twl_remap_pages, pools, table, lens, self.num_phys_pages,
+                      parent, reserve, sinks, window, self.ws, stream)
+        # a call's outcome follows from table, lengths and arguments alone: it is the same for all
+        for pools in self._further():
+            with launch_stream(self.device, stream):
+                for copy, of in zip(self._copies, (self.page_table, self.seq_lens)):
+                    copy.copy_(of)
+            step(pools, *self._copies)
+        step(self.pools[:twl.TWL_MAX_POOLS], self.page_table, self.seq_lens)
 
     def compact(self, table_out=None, stream=None):
         """Moves the used pages to the front of the pools.  The table with the new numbers goes to
@@ -366,9 +382,18 @@ class PageManager:
         if table_out is None:
             table_out = self.page_table
         expect_tensor("table_out", table_out, self.page_table.shape, torch.int32, self.device)
-        on_device(self.device, twl.twl_compact_pages, self.pools, self.page_table, table_out,
-                  self.num_phys_pages, self.num_used, self.ws, stream)
+        def step(pools, out):
+            on_device(self.device, twl.twl_compact_pages, pools, self.page_table, out,
+                      self.num_phys_pages, self.num_used, self.ws, stream)
+        for pools in self._further():
+            step(pools, self._copies[0])
+        step(self.pools[:twl.TWL_MAX_POOLS], table_out)
         return self.num_used
+
+    def _further(self):
+        """The pools behind those of one call, in lists that a call takes."""
+        n = twl.TWL_MAX_POOLS
+        return [self.pools[i:i + n] for i in range(n, len(self.pools), n)]
 
     def status(self, clear: bool = False, stream=None):
         """(status, flags) of the device flags, behind the calls issued on `stream`, which it

@@ -439,6 +439,9 @@ twl_status twl_int4_decode(const void* q, int32_t num_q_heads, const twl_int4_kv
  *   the i-th used page at or above *num_used goes to the i-th free page below it, in every pool.
  *   page_table_out (may be page_table) gets the table with the new numbers.  An entry
  *   >= num_phys_pages raises TWL_FLAG_BAD_INDEX and nothing is changed.
+ * Both follow from the table, lengths and arguments alone: with more than TWL_MAX_POOLS pools, call
+ *   for the further ones first, on copies of page_table and seq_lens (compaction: with another
+ *   page_table_out), and for the first ones on the table itself.
  * Both: page_table int32 [batch][max_pages], seq_lens int32 [batch], 1 <= num_pools <=
  *   TWL_MAX_POOLS, workspace TWL_OP_PAGES (batch, max_pages), zeroed once;
  *   batch > 4096 or num_phys_pages > 8388608 (2^23): TWL_ERR_UNSUPPORTED.  One cooperative launch

@@ -448,3 +448,54 @@ def test_host_threads_with_calls_of_different_sizes(call):
     assert failed == []
     for job in jobs:
         assert all(torch.equal(x, y) for x, y in zip(job[4], job[5]))
+
+
+# ------------------------------------------------------------------ pools
+def test_a_manager_refuses_pools_when_it_is_made():
+    from adaptive_top_sparse_b200.layer import PageManager
+    e = lambda *s, dt=torch.float16: torch.empty(s, dtype=dt, device="meta")
+    table, lens = e(3, 5, dt=torch.int32), e(3, dt=torch.int32)
+    for pool in (e(4, 3), e(4), e(4, 0), e(0, 8), e(4, 2, 17, dt=torch.uint8)):
+        with pytest.raises(ValueError):
+            PageManager([e(pool.shape[0], 8), pool], table, lens)
+
+
+@pytest.mark.gpu
+def test_a_manager_of_as_many_pools_as_layers_have():
+    """300 pools step and compact as one pool whose page holds all of theirs does; a step that
+    cannot be carried out changes none of them."""
+    from adaptive_top_sparse_b200.layer import PageManager
+    count, lens = 300, [40, 17, 0, 300]
+    table, n, pages = _deal(lens, 4, extra_pages=2, spare=20)
+    whole = torch.arange(pages * count * 4, dtype=torch.int32, device="cuda").view(pages, count, 4)
+    pools = [whole[:, i].contiguous() for i in range(count)]
+    one = PageManager([whole], table.clone(), n.clone())
+    many = PageManager(pools, table, n)
+
+    def same():
+        return torch.equal(one.page_table, many.page_table) and torch.equal(one.seq_lens, many.seq_lens) \
+            and torch.equal(whole, torch.stack(pools, 1)) and one.status() == many.status()
+    side = torch.cuda.Stream()
+    for parent, stream in (([0, 0, 0, 3], None), ([1, 1, 3, 0], side), ([0, 1, 2, -1], None)):
+        reserve = torch.tensor([1, 16, 5, 40], dtype=torch.int32, device="cuda")
+        parent = torch.tensor(parent, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        for m in (one, many):
+            m.remap(parent, reserve, 4, 1000, stream=stream)
+        torch.cuda.synchronize()
+        assert same() and one.status() == (0, 0)
+    out = [torch.empty_like(table) for _ in range(2)]
+    for m, x in ((one, out[0]), (many, out[1])):
+        assert int(m.compact(x)) > 0
+        m.page_table.copy_(x)
+    assert same() and int(one.num_used) == int(many.num_used)
+    many.page_table[0, 0] = one.page_table[0, 0] = 0 if int(table[0, 0]) else 1
+    for m in (one, many):
+        m.compact()
+    assert same() and one.status() == (0, 0)
+    before = whole.clone(), table.clone(), n.clone()
+    reserve.fill_(PAGE * (pages + 1))
+    for m in (one, many):
+        m.remap(parent, reserve)
+    assert many.status() == one.status() != (0, 0)
+    assert same() and all(torch.equal(x, y) for x, y in zip(before, (whole, table, n)))
