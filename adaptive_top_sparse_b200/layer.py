@@ -106,6 +106,7 @@ class DecodeLayer:
         # of one shape whose calls run in order on one stream can share it
         self.ws_prefill = None
         self._pages = None
+        self._centroids = None
 
     @classmethod
     def from_workload(cls, wl, device="cuda"):
@@ -201,10 +202,12 @@ class DecodeLayer:
 
     # ------------------------------------------------------------------ pages
     def pages(self) -> "PageManager":
-        """The page manager of this layer's cache and its derived K data (built on first use)."""
+        """The page manager of this layer's cache and its derived K data, the centroids of the
+        two-level path among it once they exist (built on first use)."""
         if self._pages is None:
+            more = [] if self._centroids is None else [self._centroids]
             self._pages = PageManager([self.k, self.v, self.aux.k_int4, self.aux.k_scale_zero,
-                                       self.aux.bounds], self.page_table, self.seq_lens)
+                                       self.aux.bounds, *more], self.page_table, self.seq_lens)
         return self._pages
 
     def expect_query(self, q) -> None:
@@ -215,6 +218,16 @@ class DecodeLayer:
     def staged(self) -> "Staged":
         """The same step as five separate library calls (see Staged)."""
         return Staged(self)
+
+    def centroids(self):
+        """fp16 [num_phys_pages][num_kv_heads][128], made on first use: page centroids, filled by
+        DoubleP.build_centroids.  They move and fork with their pages."""
+        if self._centroids is None:
+            self._centroids = torch.zeros((self.k.shape[0], self.num_kv_heads, 128),
+                                          dtype=torch.float16, device=self.device)
+            if self._pages is not None:
+                self._pages.add(self._centroids)
+        return self._centroids
 
     def double_p(self) -> "DoubleP":
         """The two-level top-p path on this layer's cache (built on first use)."""
@@ -338,22 +351,38 @@ class PageManager:
         if not pools or not all(isinstance(t, torch.Tensor) and t.dim() >= 1 for t in pools):
             raise ValueError("pools: expected tensors [num_phys_pages][...]")
         dev, p_phys = pools[0].device, pools[0].shape[0]
+        self.device, self.num_phys_pages = dev, p_phys
         for t in pools:
-            expect_tensor("pool", t, (p_phys, *t.shape[1:]), t.dtype, dev)
-            if t.nbytes == 0 or t.nbytes // p_phys % 16 or (dev.type != "meta" and t.data_ptr() % 16):
-                raise ValueError("pool: expected pages of a multiple of 16 bytes, 16-byte aligned, "
-                                 f"got {t.nbytes} bytes in {p_phys} pages")
+            self._expect_pool(t)
         expect_table(page_table, seq_lens, dev)
         self.pools, self.page_table, self.seq_lens = pools, page_table, seq_lens
-        self.device, self.num_phys_pages = dev, p_phys
         self.batch, self.max_pages = page_table.shape
         self.num_used = torch.zeros((), dtype=torch.int32, device=dev)
         # table and lengths that the calls for pools behind the first TWL_MAX_POOLS work on
         self._copies = None
-        if len(pools) > twl.TWL_MAX_POOLS:
-            self._copies = torch.empty_like(page_table), torch.empty_like(seq_lens)
+        self._make_copies()
         self.ws = twl.alloc_workspace(twl.TWL_OP_PAGES, dev, batch=self.batch,
                                       max_pages=self.max_pages, rows=p_phys)
+
+    def _expect_pool(self, t) -> None:
+        p_phys = self.num_phys_pages
+        expect_tensor("pool", t, (p_phys, *t.shape[1:]), t.dtype, self.device)
+        if t.nbytes == 0 or t.nbytes // p_phys % 16 or (not t.is_meta and t.data_ptr() % 16):
+            raise ValueError("pool: expected pages of a multiple of 16 bytes, 16-byte aligned, "
+                             f"got {t.nbytes} bytes in {p_phys} pages")
+
+    def _make_copies(self) -> None:
+        if len(self.pools) > twl.TWL_MAX_POOLS and self._copies is None:
+            self._copies = torch.empty_like(self.page_table), torch.empty_like(self.seq_lens)
+
+    def add(self, pool) -> None:
+        """One more pool [num_phys_pages][...] that the table indexes, from the next call on (a
+        captured call keeps the pools it was captured with)."""
+        if not isinstance(pool, torch.Tensor) or pool.dim() < 1:
+            raise ValueError("pool: expected a tensor [num_phys_pages][...]")
+        self._expect_pool(pool)
+        self.pools.append(pool)
+        self._make_copies()
 
     def remap(self, parent, reserve=None, sinks: int = 0, window: int = ALL_TOKENS,
               stream=None) -> None:
@@ -412,7 +441,7 @@ class DoubleP:
         L, dev = layer, layer.device
         b, hq, hkv, mp = L.batch, L.num_q_heads, L.num_kv_heads, L.max_pages
         i32, f32 = torch.int32, torch.float32
-        self.centroids = torch.zeros((L.k.shape[0], hkv, 128), dtype=torch.float16, device=dev)
+        self.centroids = L.centroids()
         self.sel = torch.full((b, hq, mp), -1, dtype=i32, device=dev)
         self.sel_count = torch.zeros((b, hq), dtype=i32, device=dev)
         self.cluster_w = torch.zeros((b, hq, mp), dtype=f32, device=dev)

@@ -458,6 +458,12 @@ def test_a_manager_refuses_pools_when_it_is_made():
     for pool in (e(4, 3), e(4), e(4, 0), e(0, 8), e(4, 2, 17, dt=torch.uint8)):
         with pytest.raises(ValueError):
             PageManager([e(pool.shape[0], 8), pool], table, lens)
+    m = PageManager.__new__(PageManager)
+    m.device, m.num_phys_pages, m.pools = table.device, 4, []
+    for pool in (None, e(5, 8), e(4, 3), e(4, 8, 2).transpose(1, 2), torch.zeros(4, 8)):
+        with pytest.raises(ValueError):
+            m.add(pool)
+    assert m.pools == []
 
 
 @pytest.mark.gpu
@@ -499,3 +505,32 @@ def test_a_manager_of_as_many_pools_as_layers_have():
         m.remap(parent, reserve)
     assert many.status() == one.status() != (0, 0)
     assert same() and all(torch.equal(x, y) for x, y in zip(before, (whole, table, n)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("manager_first", [False, True])
+def test_centroids_follow_their_pages(manager_first):
+    """After forks, frees and a compaction the two-level path reads what centroids built anew hold,
+    whether its buffers were made before the manager or behind it."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer
+    table, n, pages = _deal([300, 45, 70, 160], 3, extra_pages=2, spare=30)
+    k, v = _rand(1, pages, 2, PAGE, D), _rand(2, pages, 2, PAGE, D)
+    layer, q = DecodeLayer(k, v, table, n, 8, 2), _rand(3, 4, 8, D)
+    if manager_first:
+        layer.pages()
+    dp = layer.double_p()
+    layer.build_aux()
+    dp.build_centroids()
+    used = lambda: layer.page_table[layer.page_table >= 0].unique().long()
+    for parent in ([0, 0, 2, 0], [1, 1, -1, 3]):
+        layer.pages().remap(torch.tensor(parent, dtype=torch.int32, device="cuda"))
+        layer.pages().compact()
+        n.copy_(torch.where(n == 0, 1, n))             # the freed slot: one token, on no page
+        o, lse = (x.clone() for x in dp.decode(q))
+        kept = dp.centroids[used()].clone()
+        dp.build_centroids()
+        assert torch.equal(kept, dp.centroids[used()])
+        o2, lse2 = dp.decode(q)
+        live = [b for b, p in enumerate(parent) if p >= 0]
+        assert torch.equal(o[live], o2[live]) and torch.equal(lse[live], lse2[live])
+    assert layer.pages().status() == (0, 0)
