@@ -45,6 +45,11 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kSlack = 8.f;  // log2: a row's maximum is raised only when exceeded by more
+// Up to here a score is scaled and its maximum taken off in one fma.  The maximum is rounded, so all
+// weights of a row share a factor of up to 2^(2^-24 kFar): nothing that o or lse sees.  Beyond, that
+// factor would pass fp16's range: there scores in TMEM are first scaled, rounded as their maximum
+// is, brought to it and scaled back.
+constexpr float kFar = 0x1p20f;
 constexpr int kRows = 256, kTileRows = 128, kKeys = 128;
 constexpr int kThreads = 640;
 constexpr int kBufBytes = 32768, kBufs = 5;
@@ -318,6 +323,23 @@ __device__ __forceinline__ void hide(uint32_t (&v)[32], uint32_t seen) {
   for (int k = 0; k < 32; ++k) v[k] = seen >> k & 1u ? v[k] : 0xFF800000u;
 }
 __device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+// Brings 64 columns of scores that lie far from 0 to their row's maximum (see kFar).
+__device__ __noinline__ void far_scores(uint32_t ts, float scale, float ref) {
+  const float back = 1.f / scale;
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 16) {
+    uint32_t s[16];
+    tmem_ld16(s, ts + c);
+    wait_ld();
+    keep_ld16(s);
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      s[k] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(s[k]), scale), ref) * back);
+    tmem_st16(ts + c, s);
+  }
+  wait_st();
+}
 
 // ------------------------------------------------------------------ the flat list
 struct Chunk {
@@ -931,7 +953,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         const float top = max2(m0, *other) * a.scale_log2;
-        if (__any_sync(0xffffffffu, !(top <= m + kSlack))) {
+        // (a difference: of two large numbers it is exact, and of two -inf NaN, a raise to -inf)
+        if (__any_sync(0xffffffffu, !(top - m <= kSlack))) {
           // a row that has seen a score of NaN or +inf is NaN from here on: sum, lse and all of o
           float mn = max2(m, top);
           if (mn == INFINITY) mn = NAN;
@@ -952,7 +975,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float ref = ref_of(m);
-        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), shift2 = pack2(-ref, -ref);
+        float shift = -ref;
+        if (__any_sync(0xffffffffu, fabsf(ref) > kFar)) {
+          wait_ld();
+          far_scores(ts, a.scale_log2, ref);  // (inline it takes 2 % of a prompt, called nothing)
+          tmem_ld32(v, ts);
+          shift = 0.f;
+        }
+        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), shift2 = pack2(shift, shift);
         uint64_t sum = 0;
 #pragma unroll 1
         for (int c = 0; c < 64; c += 32) {

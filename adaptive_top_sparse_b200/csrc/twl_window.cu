@@ -586,8 +586,9 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
             for (int r = 0; r < 2; ++r)
               if (!sees(0, r)) x[0][2 * r] = x[0][2 * r + 1] = -INFINITY;
           }
-          if (__any_sync(0xffffffffu, fmaxf(x[0][0], x[0][2]) > st.m[0] + kSlack ||
-                                          fmaxf(x[0][1], x[0][3]) > st.m[1] + kSlack))
+          // (as differences: those of large numbers are exact)
+          if (__any_sync(0xffffffffu, fmaxf(x[0][0], x[0][2]) - st.m[0] > kSlack ||
+                                          fmaxf(x[0][1], x[0][3]) - st.m[1] > kSlack))
             raise_max(st, x[0]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {

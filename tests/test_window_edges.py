@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from adaptive_top_sparse_b200 import twl
-from test_window import ALL, D, PAGE, _attend, _check, _deal, _rand, _rows, _seen
+from test_window import ALL, D, PAGE, _attend, _check, _deal, _rand, _rows, _seen, _unquantise
 
 
 @pytest.mark.gpu
@@ -534,3 +534,47 @@ def test_centroids_follow_their_pages(manager_first):
         live = [b for b, p in enumerate(parent) if p >= 0]
         assert torch.equal(o[live], o2[live]) and torch.equal(lse[live], lse2[live])
     assert layer.pages().status() == (0, 0)
+
+
+# ------------------------------------------------------------------ limits
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [2.0 ** e for e in range(0, 16, 3)] + [30000.0, 60000.0])
+def test_scores_up_to_the_largest_of_fp16_rows(size):
+    """Rows of one repeated value, so that scores are +-128 size x: 2^4 up to 2^36 in log2 units, and
+    next to one another at every distance.  One token, fp16 and in 4 bits (which hold such rows
+    exactly), and chunks, units of one and two query tiles.
+
+    Tolerances: scores are exact sums (128 equal products), their scaling rounds once (2^-24 of the
+    score, on both sides of a difference), so a weight that is not 0 or 1 is off by at most
+    2^-22 |score| in log2 units; such weights only count where scores lie within 40 of one another."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer, Int4Layer
+    n, hq, hkv = 900, 4, 2
+    table, lens, pages = _deal([n], 5)
+    g = torch.Generator().manual_seed(int(size))
+    steps = torch.randint(-8, 9, (pages, hkv, PAGE, 1), generator=g)
+    k = (size * (1 + steps / 1024) * torch.sign(steps + 0.5)).expand(-1, -1, -1, D)
+    k = k.contiguous().half().cuda()
+    v = _rand(2, pages, hkv, PAGE, D)
+    for qn in (300, 3):
+        sign = torch.where(torch.arange(qn * hq) % 3 == 0, -1.0, 1.0).view(qn, hq, 1)
+        q = (sign * size).expand(-1, -1, D).contiguous().half().cuda()
+        start = torch.tensor([0, qn], dtype=torch.int32, device="cuda")
+        layer = DecodeLayer(k, v, table, lens, hq, hkv)
+        o, lse = layer.window_prefill(q, start, 0, 700)
+        one, lse1 = layer.window_decode(q[-1:].contiguous(), 0, 700)
+        t = torch.arange(n - qn, n, device="cuda")
+        want, wlse, big = _attend(q.double(), _rows(k, table, 0, n).double(),
+                                  _rows(v, table, 0, n).double(), _seen(t, n, 0, 700))
+        # an error of e in the exponents moves o by at most e max|v| (weights sum to 1)
+        off = min(2.0, 2.0 ** -22 * big * 1.5) if 128 * size * size / 1024 * 0.08 < 40 else 0.0
+        assert (o.double() - want).abs().max().item() <= (3 * 2.0 ** -11 + off) * 6.0
+        assert (one.double() - want[-1:]).abs().max().item() <= (2.0 ** -17 + off) * 6.0
+        assert (lse.double() - wlse).abs().max().item() <= 2.0 ** -18 * (1 + big)
+        assert (lse1.double() - wlse[-1:]).abs().max().item() <= 2.0 ** -18 * (1 + big)
+        four = Int4Layer.from_fp16(k, v, table, lens, hq, hkv)
+        one, lse1 = four.decode(q[-1:].contiguous(), window=700)
+        vv = _unquantise(_rows(four.v, table, 0, n), _rows(four.v_sz, table, 0, n))
+        want, wlse, big = _attend(q[-1:].double(), _rows(k, table, 0, n).double(), vv,
+                                  _seen(t[-1:], n, 0, 700))
+        assert (one.double() - want).abs().max().item() <= (2.0 ** -17 + off) * 6.0
+        assert (lse1.double() - wlse).abs().max().item() <= 2.0 ** -18 * (1 + big)
