@@ -91,9 +91,13 @@ twl_status check_budget(int budget_pages, int budget_div, int max_budget, int ma
   return TWL_OK;
 }
 
-// Arguments of attention under a window with sinks.
+// Arguments of attention under a window with sinks.  |q.k| is below 2^43 for rows of up to
+// 16 x 65504 (4-bit ones), so the largest scale keeps scores far inside fp32 and above the one-token
+// kernel's lowest maximum.
+constexpr float kMaxScale = 0x1p48f;
 twl_status check_window(int sinks, int window, float sm_scale) {
-  if (sinks < 0 || window < 1 || !(sm_scale > 0.f) || isinf(sm_scale)) return TWL_ERR_INVALID_ARG;
+  if (sinks < 0 || window < 1 || !(sm_scale > 0.f) || sm_scale > kMaxScale)
+    return TWL_ERR_INVALID_ARG;
   return TWL_OK;
 }
 

@@ -42,7 +42,7 @@ constexpr float kSlack = 8.f;
 // Where a 4-bit code meets the tensor core as fp16 (see k_window_decode): two per word.
 constexpr uint32_t kNibble = 0x00F000F0u;
 // The maximum of a head that has seen nothing: finite, so that no difference with it is NaN, and
-// below every score of fp16 rows.
+// below every finite score (2^92 at the largest scale, in magnitude).
 constexpr float kNone = -1e30f;
 constexpr int kAlignedBatch = 160;
 constexpr int kJoinTiles = 24;

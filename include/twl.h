@@ -344,7 +344,7 @@ twl_status twl_sparse_decode_noalloc(const void* q, int32_t num_q_heads, const t
  * queries that see it: a K row all of their o, a V row the columns that are not finite (in a chunk
  * as NaN; where a block of 256 / (Hq / Hkv) queries sees more than two such rows in part, the
  * columns of the further ones may be NaN for all of its queries that see the first).  sm_scale must
- * be positive and finite.
+ * be positive and at most 2^48.
  *
  * twl_window_decode: one token per sequence, the last one (t = seq_lens[b] - 1; it is in the
  *   cache already, see twl_append_token).

@@ -578,3 +578,39 @@ def test_scores_up_to_the_largest_of_fp16_rows(size):
                                   _seen(t[-1:], n, 0, 700))
         assert (one.double() - want).abs().max().item() <= (2.0 ** -17 + off) * 6.0
         assert (lse1.double() - wlse).abs().max().item() <= 2.0 ** -18 * (1 + big)
+
+@pytest.mark.parametrize("scale", [2.0 ** 48 * (1 + 2.0 ** -20), 1e30, 3e38, -1.0, 0.0])
+def test_scales_out_of_range_are_refused(scale):
+    """Above 2^48 a score of fp16 or 4-bit rows could pass the kernels' lowest maximum (-1e30):
+    |q.k| < 2^43 for rows of up to 16 x 65504, so scores in log2 units stay below 2^92."""
+    from test_window import _decode, _decode4, _prefill
+    for call in (_decode, _prefill, _decode4):
+        assert call(scale=scale) == twl.TWL_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+def test_the_largest_scale():
+    """Scores of up to 2^48 |q.k|: one key wins, whatever the sign of its score."""
+    from adaptive_top_sparse_b200.layer import DecodeLayer, Int4Layer
+    table, n, pages = _deal([1, 300], 3)
+    k, v, q = _rand(1, pages, 2, PAGE, D), _rand(2, pages, 2, PAGE, D), _rand(3, 2, 8, D)
+    first = k[table[0, 0], :, 0].float()                       # the only key of sequence 0
+    q[0] = (-q[0].float() * (q[0].float().view(2, 4, D) @ first[..., None]).sign().view(8, 1)).half()
+    scale, start = 2.0 ** 48, torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    layer, four = DecodeLayer(k, v, table, n, 8, 2), Int4Layer.from_fp16(k, v, table, n, 8, 2)
+    half, lse = torch.empty_like(q), torch.empty((2, 8), device="cuda")
+    layer.window_prefill(q, start, out=(half, lse))
+    twl.twl_window_decode(q, 8, layer.kv, 0, ALL, scale, layer.o, layer.lse, layer.ws_window)
+    twl.twl_int4_decode(q, 8, four.kv, None, None, False, 0, ALL, scale, four.o, four.lse, four.ws)
+    twl.twl_window_prefill(q, start, 2, 8, layer.kv, 0, ALL, scale, half, lse, layer.ws_prefill)
+    for b, m in enumerate((1, 300)):
+        fp16 = [_rows(x, table, b, m).double() for x in (k, v)]
+        int4 = [_unquantise(_rows(c, table, b, m), _rows(z, table, b, m))
+                for c, z in ((four.k, four.k_sz), (four.v, four.v_sz))]
+        for o, l, (kk, vv), u in ((layer.o, layer.lse, fp16, 2.0 ** -17), (half, lse, fp16, 3 * 2.0 ** -11),
+                                  (four.o, four.lse, int4, 2.0 ** -17)):
+            s = torch.einsum("hd,thd->ht", q[b].double(), kk.repeat_interleave(4, 1)) * scale
+            assert (l[b].double() - s.amax(1)).abs().max() <= 2.0 ** -18 * s.abs().max()
+            best = vv.repeat_interleave(4, 1)[s.argmax(1), torch.arange(8, device="cuda")]
+            assert (o[b].double() - best).abs().max().item() <= u * 6.0
+            assert b == 1 or bool((s < 0).all())
