@@ -28,11 +28,14 @@
 // and accumulators are fp32.  Waits are bounded: one that gives up raises TWL_FLAG_TIMEOUT and
 // the CTA leaves without its outputs.
 //
-// Measured (one B200, 32/8 heads): a prompt of 8192 under a window of 2048 in 327 us (737 TFLOP/s),
-// four chunks of 1.5K-2K over 2K-8K cached tokens in 614 us (902 TFLOP/s, 55 % of the measured bf16
-// rate), 1-8 drafted tokens behind eight contexts in 43 us (3.1 TB/s).  Bound: a query tile's chain
-// (some 2100 cycles of softmax, 1100 of products, and the hand-overs) is longer than the other
-// tile's 1072 cycles of the tensor core; TMEM has no room for a third tile of scores.
+// Measured (one B200, 32/8 heads; replays of a graph in short bursts, and in brackets passes back to
+// back): a prompt of 8192 under a window of 2048 in 327 (357) us (736, 675 TFLOP/s), four chunks of
+// 1.5K-2K over 2K-8K cached tokens in 607 (691) us (912, 801 TFLOP/s, 56 and 49 % of the measured bf16
+// rate; the power cap takes part of it), 1-8 drafted tokens behind eight contexts in 44 us (3.0 TB/s).
+// Bound: the chain of a query tile (some 2100 cycles of softmax, 1100 of products, and the hand-overs)
+// is longer than the other tile's 1072 cycles of the tensor core.  TMEM has no room for a third tile
+// of scores; the softmax has 96 registers a thread (640 equal threads), so it reads each score from
+// TMEM twice, and the halves of a row meet through shared memory in every tile.
 #include <cuda.h>
 
 #include "twl_common.cuh"
@@ -56,6 +59,10 @@ constexpr int kBufBytes = 32768, kBufs = 5;
 constexpr int kQBytes = 65536;
 // What a unit costs beside its key tiles (filling and emptying the pipeline, masks, the output), in
 // tiles: places in the flat list that hold no work, so that a run of many short units is shorter.
+// Measured with 0, 1, 2 and 3 (us, 32/8 heads but for the last two): 8 x 1-8 tokens behind 2-8K under
+// 4096 42.5, 41.3, 41.5, 41.6; prompt of 8K under 2048 328, 306, 306, 306; four chunks of 1.5-2K over
+// 2-8K 570, 544, 545, 544; 32 chunks of 64 behind 1-4K 138, 144, 138, 138; 64 prompts of 16-400 156,
+// 167, 169, 169; 1K, 64/8 heads, 65, 68, 68, 68; 16K, 8/1 heads, 662, 580, 574, 577.
 constexpr int kUnitCost = 2;
 constexpr int kRecs = 8;
 constexpr int kSpoils = 16, kSpoilsPer = 4;  // of the CTA's last segments; of one (two a fixer)

@@ -21,9 +21,11 @@
 // barrier in the loop), with transposed products so that the <= 8 heads of a group are the N = 8
 // of mma.m16n8k16:  S^T = K Q^T (16 tokens x 8 heads), O^T = V^T P^T (16 dims x 8 heads); P^T
 // comes from S^T by an 8x8 transpose in registers (movmatrix).
-// Measured (one B200): 16 sequences of 8K-32K tokens, fp16, 204 us (6.2 TB/s, the copy rate is
-// 6.55); 64 x 8K tokens of a 4-bit cache 181 us (3.2 TB/s: 398 instructions a page, half of them
-// the codes' extraction, bound it; 12 warps with two pages a step against 16 with one: 181, 185 us).
+// Measured (one B200): 16 sequences of 8K-32K tokens, fp16, 205 us (6.15 TB/s, the copy rate is
+// 6.55); 64 x 8K tokens of a 4-bit cache 183 us (3.1 TB/s).  There no unit is full (issue slots 52 %,
+// ALU 50 %, DRAM 40 %, tensor 18 %): the bound is the latency of a warp's chain of scores, maximum,
+// weights, transpose and V, 398 instructions a page, with 12 warps an SM (167 registers a thread; 12
+// warps with two pages a step against 16 with one: 181, 185 us).
 // Precision: o and lse are fp32 results, so P enters as hi + lo fp16 parts (22 bits).  With G <= 4
 // the parts use the two halves of the N = 8 columns and cost nothing; G = 8 takes two products.
 #include "twl_common.cuh"
@@ -44,6 +46,14 @@ constexpr uint32_t kNibble = 0x00F000F0u;
 // The maximum of a head that has seen nothing: finite, so that no difference with it is NaN, and
 // below every finite score (2^92 at the largest scale, in magnitude).
 constexpr float kNone = -1e30f;
+// Runs that stay inside one group (see the kernel): tried for batches up to here, as a longer one
+// cannot have a run for each sequence (148 SMs), and taken if the longest run is at most this many
+// tiles longer than an equal share.  Measured on both sides, groups of 4 heads, 8 to 144 groups of 512
+// to 32K tokens, equal and ragged, against runs of equal length:
+//   tiles more   fp16 (16 tokens a tile)   4 bits (32)
+//   up to 24     3-40 % faster             6-50 % faster
+//   25 to 60     11 % faster to 3 % slower 28 % faster to 1 % slower
+//   65 and more  5-80 % slower             3-60 % slower
 constexpr int kAlignedBatch = 160;
 constexpr int kJoinTiles = 24;
 constexpr int kPartStride = 132;  // floats of one head's partial: o[128], max, sum, pad
@@ -214,7 +224,7 @@ __device__ __forceinline__ float max4(const float (&v)[4]) {
   return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
 }
 
-// P^T fragments (hi and lo parts) of the weights w (same order as t in update_max).
+// P^T fragments (hi and lo parts) of the weights w (same order as t in raise_max).
 template <int G>
 __device__ __forceinline__ void p_fragments(const float (&w)[4], bool low, uint32_t (&hi)[2],
                                             uint32_t (&lo)[2]) {
@@ -280,8 +290,7 @@ __global__ void __launch_bounds__(Cfg<INT4>::kWarps * 32, 1)
                  max((total + kWarps - 1) / kWarps, a.batch * a.hkv));
   // With few groups every run stays inside one: sequence b's groups get whole numbers of runs in
   // proportion to their tiles.  The longest run may then be longer than an equal share, but no CTA
-  // joins twice; a second join costs about as much time as kJoinTiles tiles (measured with 128
-  // groups of 126 tiles of 4-bit rows: 34.7 against 39.8 us).
+  // joins twice; a second join costs about as much time as kJoinTiles tiles.
   bool aligned = false;
   if (a.batch <= kAlignedBatch && total > 0) {
     const int t = tid < a.batch ? prefix[tid + 1] - prefix[tid] : 0;

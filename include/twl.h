@@ -338,11 +338,13 @@ twl_status twl_sparse_decode_noalloc(const void* q, int32_t num_q_heads, const t
  * hold, stay visible): the query at position t of its sequence sees key j iff
  *   j <= t  and  (j < sinks or j > t - window).
  * sinks >= 0, window >= 1; window = INT32_MAX sees every token.  o = softmax(sm_scale q K^T) V
- * over the seen keys (fp16 K/V, fp32 sums), lse = natural-log sum of exp of the scaled scores.
+ * over the seen keys (fp16 K/V; scores, maxima and sums in fp32; for the product with V a weight
+ * keeps 22 bits in the calls of one token, whose o is fp32, and 11 in chunks, whose o is fp16: there
+ * o is within 3 2^-11 max|v|), lse = natural-log sum of exp of the scaled scores.
  * Only pages that hold a seen key are read: the table may have -1 for the others.  K and V rows
  * nobody sees may hold anything (NaN included), and a row that is not finite reaches only the
- * queries that see it: a K row all of their o, a V row the columns that are not finite (in a chunk
- * as NaN; where a block of 256 / (Hq / Hkv) queries sees more than two such rows in part, the
+ * queries that see it: a K row all of their o (unless its score is -inf, a weight of 0), a V row the
+ * columns that are not finite (in a chunk as NaN; where a block of 256 / (Hq / Hkv) queries sees more than two such rows in part, the
  * columns of the further ones may be NaN for all of its queries that see the first).  sm_scale must
  * be positive and at most 2^48.
  *
@@ -359,7 +361,7 @@ twl_status twl_sparse_decode_noalloc(const void* q, int32_t num_q_heads, const t
  *   sits at position seq_lens[b] - q_len_b + i; its K and V are in the cache already.
  *   q float16 [total_q][Hq][128]; q_start int32 [B + 1], ascending from >= 0 to <= total_q
  *   o float16 [total_q][Hq][128] out, 32-byte aligned; lse float [total_q][Hq] out
- *   Rows of q outside every chunk are not read and their outputs not written.  q_len_b = 0 is
+ *   Rows of q outside every chunk may hold anything; their outputs are not written.  q_len_b = 0 is
  *   fine.  A sequence whose chunk is not inside [0, total_q] or longer than its length, or whose
  *   length is > 16 * max_pages, is skipped (its outputs are not written), and a page that is out
  *   of range is skipped, both with TWL_FLAG_BAD_INDEX.  total_q = 0 launches nothing.
@@ -383,7 +385,7 @@ twl_status twl_window_prefill(const void* q, const int32_t* q_start, int32_t tot
  *   quantised and written to position n_b = seq_lens[b], which the caller has mapped, and query b
  *   at t = n_b attends over the n_b + 1 tokens, the new one's quantised row among them, under the
  *   window and sinks of twl_window_decode; with both NULL nothing is written and t = n_b - 1.
- *   Scores and sums are those of the rows x = code * scale + zero.  If advance != 0 (with k_new
+ *   Scores and sums are those of the rows x = code * scale + zero (scale >= 0).  If advance != 0 (with k_new
  *   only), seq_lens[b] becomes n_b + 1 behind the last read, in the same launch.
  *   q, o, lse as twl_window_decode.  An empty slot (n_b = 0, and with k_new an unmapped first
  *   page, table entry -1) gives o = 0, lse = -inf and is left alone; a position that has no
@@ -425,7 +427,8 @@ twl_status twl_int4_decode(const void* q, int32_t num_q_heads, const twl_int4_kv
  *     position n on sees under (sinks, window): they are dropped (-1);
  *   - a last page that is partly filled is shared by nobody: it stays with the parent's own slot
  *     if that continues itself, else with its lowest fork; every other fork gets a copy of it,
- *     in every pool, in a new page;
+ *     in every pool, in a new page (the given table must name it for one slot only: a caller who
+ *     sets a length back does so into pages that no other slot holds);
  *   - pages j < ceil((n + reserve[b]) / 16) behind that are kept if slot b goes on itself and has
  *     them, else new;
  *   - every other entry becomes -1, seq_lens[b] becomes n (0 for a freed slot).
