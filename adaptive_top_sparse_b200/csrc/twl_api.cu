@@ -747,6 +747,7 @@ void twl_test_set_waits(uint32_t max_polls, int32_t stall_estimate) {
   step::set_test_waits(max_polls, stall_estimate);
   step256::set_test_waits(max_polls, stall_estimate);
   prefill::set_test_waits(max_polls, stall_estimate);
+  pages::set_test_waits(max_polls, stall_estimate);
 }
 
 }  // extern "C"

@@ -22,7 +22,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPiece = 4096;           // bytes a warp copies at a time
 constexpr int kGroupWords = 8;         // bitmap words per prefix entry (256 pages)
-constexpr unsigned kSpinLimit = 1u << 24;
+constexpr unsigned kSpinLimit = 1u << 24;  // polls (Args.wait_limit)
 enum { kArrive = 0, kError = 1, kExit = 2, kSyncWords = 4 };
 constexpr unsigned kNoPages = 1u << 30;
 
@@ -37,12 +37,13 @@ __device__ unsigned grid_barrier(const Args& a, unsigned mine, unsigned* sh) {
     __threadfence();
     atomicAdd(a.sync + kArrive, 1u);
     unsigned seen = 0, polls = 0;
+    const unsigned all = gridDim.x + a.stall;
     do {
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(a.sync + kArrive));
-    } while (seen < gridDim.x && ++polls < kSpinLimit);
+    } while (seen < all && ++polls < a.wait_limit);
     __threadfence();
     unsigned e = __ldcg(a.sync + kError);
-    if (seen < gridDim.x) e |= TWL_FLAG_TIMEOUT;
+    if (seen < all) e |= TWL_FLAG_TIMEOUT;
     *sh = e;
   }
   __syncthreads();
@@ -420,18 +421,28 @@ size_t remap_smem(int batch, int num_phys) {
 }
 size_t compact_smem(int num_phys) { return ((size_t)groups_of(num_phys) + 1) * sizeof(int); }
 
+unsigned g_wait_limit = kSpinLimit;  // test knobs (twl_test_set_waits)
+unsigned g_stall = 0;
+
 // most: the kernel's need for the largest batch and pool.  The attribute is the process's, so every
 // call sets the same value: calls of other host threads never find it below their own need.
-cudaError_t launch(const void* kernel, const Args& a, const Pools& p, size_t smem, size_t most,
+cudaError_t launch(const void* kernel, Args a, const Pools& p, size_t smem, size_t most,
                    cudaStream_t s) {
+  a.wait_limit = g_wait_limit;
+  a.stall = g_stall;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return e;
-  void* args[] = {const_cast<Args*>(&a), const_cast<Pools*>(&p)};
+  void* args[] = {&a, const_cast<Pools*>(&p)};
   return cudaLaunchCooperativeKernel(kernel, dim3(num_sms()), dim3(kThreads), args, smem, s);
 }
 
 }  // namespace
+
+void set_test_waits(uint32_t max_polls, int stall) {
+  g_wait_limit = max_polls > 0 ? max_polls : kSpinLimit;
+  g_stall = stall != 0;
+}
 
 // The bitmap has room for the largest pool: what is zero between launches lies in one place whatever
 // the call's sizes, so that one workspace serves them all.

@@ -28,6 +28,8 @@ struct Args {
   int* num_used;
   int batch, max_pages, num_phys;
   int sinks, window;
+  unsigned wait_limit;  // polls before the barrier's wait gives up
+  unsigned stall;       // test of that: the barrier waits for one CTA more than there are
   // workspace
   unsigned* sync;    // [4] arrivals, error bits, exits; zero between launches
   unsigned* bitmap;  // [words] used pages; zero between launches
@@ -38,6 +40,8 @@ struct Args {
 
 size_t workspace_bytes(int batch, int max_pages);
 void carve(Args& a, void* ws);
+// Test knobs for the bounded wait (twl_test_set_waits).
+void set_test_waits(uint32_t max_polls, int stall);
 cudaError_t launch_remap(const Args& a, const Pools& p, cudaStream_t s);
 cudaError_t launch_compact(const Args& a, const Pools& p, cudaStream_t s);
 

@@ -448,7 +448,8 @@ twl_status twl_int4_decode(const void* q, int32_t num_q_heads, const twl_int4_kv
  * Both: page_table int32 [batch][max_pages], seq_lens int32 [batch], 1 <= num_pools <=
  *   TWL_MAX_POOLS, workspace TWL_OP_PAGES (batch, max_pages), zeroed once;
  *   batch > 4096 or num_phys_pages > 8388608 (2^23): TWL_ERR_UNSUPPORTED.  One cooperative launch
- *   each (every SM takes one CTA); a wait that gives up raises TWL_FLAG_TIMEOUT (state undefined). */
+ *   each (every SM takes one CTA); a wait that gives up raises TWL_FLAG_TIMEOUT (the
+ *   caller's state is undefined if only some CTAs gave up; the next launch on ws is valid). */
 #define TWL_MAX_POOLS 128
 typedef struct twl_page_pool {
   void* data;
@@ -498,15 +499,16 @@ twl_status twl_decode_step(const void* q, int32_t num_q_heads, const twl_paged_k
                            twl_stream_t stream);
 
 /* ---------------------------------------------------------------- test hook of the bounded waits
- * twl_decode_step's work items wait for one another by polling counters in the workspace, and the
- * warps of twl_window_prefill for one another in shared memory; each wait gives up after a bounded
- * number of polls, raises TWL_FLAG_TIMEOUT and aborts the launch (the kernel returns; the context
- * stays usable; the next launch on the workspace is valid).
+ * twl_decode_step's work items wait for one another by polling counters in the workspace, the
+ * CTAs of the page calls meet through one, and the warps of twl_window_prefill wait for one another
+ * in shared memory; each wait gives up after a bounded number of polls, raises TWL_FLAG_TIMEOUT and
+ * aborts the launch (the kernel returns; the context stays usable; the next launch on the workspace
+ * is valid).
  * This hook exists so that a test can make that happen without a device fault: max_polls sets
- * the polls before a wait gives up for later launches (0 = the defaults, 2^22 and, of up to 20 us
- * each, 2^16), and stall_estimate != 0 makes the INT4-estimate items, and every second CTA of a
- * chunk launch, wait for what never happens.
- * Process-wide, read at each twl_decode_step and twl_window_prefill call; not for production use. */
+ * the polls before a wait gives up for later launches (0 = the defaults: 2^22, 2^24 and, of up to
+ * 20 us each, 2^16), and stall_estimate != 0 makes the INT4-estimate items, all CTAs of a page call
+ * and every second one of a chunk launch wait for what never happens.
+ * Process-wide, read at each call of these; not for production use. */
 void twl_test_set_waits(uint32_t max_polls, int32_t stall_estimate);
 
 #ifdef __cplusplus

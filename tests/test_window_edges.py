@@ -394,6 +394,36 @@ def test_a_chunk_launch_that_gives_up_leaves_a_valid_workspace(hq, hkv, lens, qn
         assert layer.status() == (0, 0)
 
 
+@pytest.mark.gpu
+def test_a_page_call_that_gives_up_changes_nothing_and_leaves_a_valid_workspace():
+    """Through the test hook every CTA of a page call waits for one more than there are: the call
+    returns with the timeout flag, nothing has changed, and the next calls are exact."""
+    from adaptive_top_sparse_b200.layer import PageManager
+    sides = []
+    for _ in range(2):
+        table, n, pages = _deal([40, 17, 300], 4, extra_pages=2, spare=20)
+        pool = torch.arange(pages * 4, dtype=torch.int32, device="cuda").view(pages, 4)
+        sides.append((PageManager([pool], table, n), (table, n, pool)))
+    (m, mine), (ref, theirs) = sides
+    parent = torch.tensor([0, 0, 2], dtype=torch.int32, device="cuda")
+    for call, ref_call in ((lambda: m.remap(parent, parent), lambda: ref.remap(parent, parent)),
+                           (m.compact, ref.compact)):
+        before = [x.clone() for x in mine]
+        try:
+            twl.twl_test_set_waits(64, True)
+            call()
+            torch.cuda.synchronize()
+        finally:
+            twl.twl_test_set_waits(0, False)
+        assert m.status(clear=True) == (twl.TWL_ERR_TIMEOUT, twl.TWL_FLAG_TIMEOUT)
+        assert all(torch.equal(x, y) for x, y in zip(before, mine))
+        call()
+        ref_call()
+        assert m.status() == (0, 0)
+        assert all(torch.equal(x, y) for x, y in zip(mine, theirs))
+    assert int(m.num_used) == int(ref.num_used) > 0
+
+
 # ------------------------------------------------------------------ host threads
 @pytest.mark.gpu
 @pytest.mark.parametrize("call", ["decode", "int4", "remap", "compact"])
