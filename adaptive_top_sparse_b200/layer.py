@@ -177,12 +177,14 @@ class DecodeLayer:
             raise ValueError("q: expected a tensor [T][Hq][128]")
         expect_tensor("q", q, (q.shape[0], self.num_q_heads, 128), torch.float16, dev)
         expect_tensor("q_start", q_start, (self.batch + 1,), torch.int32, dev)
-        if out is None:
+        if out is None and stream is None:
+            out = (torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device=dev))
+        elif out is None:
             with launch_stream(dev, stream):
                 out = (torch.empty_like(q),
                        torch.empty(q.shape[:2], dtype=torch.float32, device=dev))
                 capturing = torch.cuda.is_current_stream_capturing()
-            if stream is not None and not capturing:
+            if not capturing:
                 for t in out:                  # the caller reads them on the current stream
                     t.record_stream(torch.cuda.current_stream(dev))
         o, lse = out
@@ -393,16 +395,15 @@ class PageManager:
         expect_tensor("parent", parent, (self.batch,), torch.int32, self.device)
         if reserve is not None:
             expect_tensor("reserve", reserve, (self.batch,), torch.int32, self.device)
-        def step(pools, table, lens):
-            on_device(self.device, twl.twl_remap_pages, pools, table, lens, self.num_phys_pages,
-                      parent, reserve, sinks, window, self.ws, stream)
+        args = self.num_phys_pages, parent, reserve, sinks, window, self.ws, stream
         # a call's outcome follows from table, lengths and arguments alone: it is the same for all
         for pools in self._further():
             with launch_stream(self.device, stream):
                 for copy, of in zip(self._copies, (self.page_table, self.seq_lens)):
                     copy.copy_(of)
-            step(pools, *self._copies)
-        step(self.pools[:twl.TWL_MAX_POOLS], self.page_table, self.seq_lens)
+            on_device(self.device, twl.twl_remap_pages, pools, *self._copies, *args)
+        on_device(self.device, twl.twl_remap_pages, self._first(), self.page_table, self.seq_lens,
+                  *args)
 
     def compact(self, table_out=None, stream=None):
         """Moves the used pages to the front of the pools.  The table with the new numbers goes to
@@ -411,16 +412,22 @@ class PageManager:
         if table_out is None:
             table_out = self.page_table
         expect_tensor("table_out", table_out, self.page_table.shape, torch.int32, self.device)
-        def step(pools, out):
-            on_device(self.device, twl.twl_compact_pages, pools, self.page_table, out,
-                      self.num_phys_pages, self.num_used, self.ws, stream)
+        args = self.num_phys_pages, self.num_used, self.ws, stream
         for pools in self._further():
-            step(pools, self._copies[0])
-        step(self.pools[:twl.TWL_MAX_POOLS], table_out)
+            on_device(self.device, twl.twl_compact_pages, pools, self.page_table,
+                      self._copies[0], *args)
+        on_device(self.device, twl.twl_compact_pages, self._first(), self.page_table, table_out,
+                  *args)
         return self.num_used
 
+    def _first(self):
+        """The pools that one call takes ..."""
+        return self.pools if self._copies is None else self.pools[:twl.TWL_MAX_POOLS]
+
     def _further(self):
-        """The pools behind those of one call, in lists that a call takes."""
+        """... and those behind them, in lists that a call takes."""
+        if self._copies is None:
+            return ()
         n = twl.TWL_MAX_POOLS
         return [self.pools[i:i + n] for i in range(n, len(self.pools), n)]
 
